@@ -1,7 +1,7 @@
 """Build libfp8sm.so (HIP, gfx950) in-tree with hipcc.
 
 Usage: python -m column_scaled_gemm_amd.build   (or __graft_entry__.build()).
-Always recompiles; objects go to _build/, the library next to this file.
+Always recompiles; objects go to _build/ (one a source under _build/parts/), the library next to this file.
 """
 import os
 import shutil
@@ -15,7 +15,15 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libfp8sm.so")
 
-SOURCES = ["quant.hip", "gemm.hip", "probe.hip", "api.cpp"]
+# object -> sources; a family of kernels in several sources is one relocatable
+# object, so whoever links the host part anew names the same few objects
+OBJECTS = {
+    "quant.o": ["quant.hip", "kv_cache.hip"],
+    "gemm.o": ["gemm.hip", "attention.hip"],
+    "probe.o": ["probe.hip"],
+    "api.o": ["api.cpp"],
+}
+SOURCES = [s for srcs in OBJECTS.values() for s in srcs]
 
 FLAGS = [
     "--offload-arch=gfx950",
@@ -54,6 +62,16 @@ def _compile(src, obj, verbose):
     return obj
 
 
+def _join(parts, obj):
+    if len(parts) == 1:
+        shutil.copy(parts[0], obj)
+        return
+    r = subprocess.run([shutil.which("ld") or "ld", "-r", "-o", obj] + parts,
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"joining {obj} failed:\n" + r.stdout + r.stderr)
+
+
 def _gen_silu_tables():
     """Compile and run the host generator of the constant SiLU tables."""
     exe = os.path.join(BUILD, "gen_silu_tables")
@@ -72,9 +90,15 @@ def _gen_silu_tables():
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     _gen_silu_tables()
-    objs = [os.path.join(BUILD, s.rsplit(".", 1)[0] + ".o") for s in SOURCES]
+    parts = os.path.join(BUILD, "parts")
+    os.makedirs(parts, exist_ok=True)
+    part = {s: os.path.join(parts, s.rsplit(".", 1)[0] + ".o") for s in SOURCES}
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        list(ex.map(lambda p: _compile(p[0], p[1], verbose), zip(SOURCES, objs)))
+        list(ex.map(lambda s: _compile(s, part[s], verbose), SOURCES))
+    objs = []
+    for name, srcs in OBJECTS.items():
+        objs.append(os.path.join(BUILD, name))
+        _join([part[s] for s in srcs], objs[-1])
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -50,6 +50,9 @@ constexpr int64_t kMaxK = 65536;
 // GEMM operand row strides (bytes): the kernels address up to 64 rows of A or
 // B with 32-bit offsets from one base, so 64 * stride + K must stay below 2^31.
 constexpr int64_t kMaxGemmLd = (int64_t)1 << 24;
+constexpr int64_t kMaxTokens = (int64_t)1 << 24;
+constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
+constexpr int32_t kMaxHeads = 1024;
 constexpr int64_t kMaxBatch = 65535;  // one grid row (blockIdx.y) per batch
 
 // Batch arguments common to every batched call: the count, non-negative
@@ -461,6 +464,194 @@ fp8sm_status fp8sm_scaled_mm_batched(int64_t nbatch, const int32_t* rows, const 
                                      hipStream_t stream) {
   return scaled_mm_impl(A, lda, B, ldb, C, ldc, M, N, K, ka, sa, kb, sb, bias, out, stream,
                         GemmBatch{nbatch, bs_a, bs_b, bs_c, bs_sa, bs_sb, rows});
+}
+
+// ---- QKV projection to attention
+
+// Checks shared by the cache calls; fills the kernels' batch and cache.
+static fp8sm_status kv_args(int64_t T, int64_t nseq, const int32_t* cu, const int32_t* lens,
+                            const int32_t* table, int64_t ld_table, int64_t max_blocks,
+                            const uint8_t* k, const uint8_t* v, const uint8_t* ke,
+                            const uint8_t* ve, int64_t num_blocks, int32_t H, int32_t D,
+                            int32_t block, KvBatch* kb, KvCache* c) {
+  if (T < 0 || nseq < 0 || H < 1 || num_blocks < 1 || max_blocks < 1) return FP8SM_ERR_SHAPE;
+  if (D != 64 && D != 128) return FP8SM_ERR_UNSUPPORTED;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return FP8SM_ERR_UNSUPPORTED;
+  if (T > kMaxTokens || nseq > kMaxSeqs || H > kMaxHeads || num_blocks > INT32_MAX ||
+      max_blocks > kMaxDim / block)
+    return FP8SM_ERR_RANGE;
+  if (ld_table < max_blocks) return FP8SM_ERR_SHAPE;
+  if (T > 0 && nseq > 0) {
+    if (!cu || !lens || !table || !k || !v || !ke || !ve) return FP8SM_ERR_NULL;
+    if (!aligned(cu, 4) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(k, 16) ||
+        !aligned(v, 16))
+      return FP8SM_ERR_ALIGN;
+  }
+  *kb = KvBatch{cu, lens, table, ld_table, (int)max_blocks, (int)T, (int)nseq};
+  c->k = const_cast<uint8_t*>(k);
+  c->v = const_cast<uint8_t*>(v);
+  c->ke = const_cast<uint8_t*>(ke);
+  c->ve = const_cast<uint8_t*>(ve);
+  c->num_blocks = (int)num_blocks;
+  c->heads = H;
+  c->D = D;
+  c->block_shift = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  return FP8SM_OK;
+}
+
+fp8sm_status fp8sm_qk_norm_rope(const void* x, fp8sm_dtype in, int64_t T, int32_t Hq, int32_t Hk,
+                                int32_t D, int64_t ld_x, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos_sin,
+                                int64_t max_pos, const int32_t* pos, int32_t rot, uint32_t flags,
+                                void* y, int64_t ld_y, hipStream_t stream) {
+  if (in != FP8SM_BF16 && in != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
+  if (flags & ~FP8SM_ROPE_INTERLEAVED) return FP8SM_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return FP8SM_ERR_UNSUPPORTED;
+  if (T < 0 || Hq < 0 || Hk < 0 || Hq + (int64_t)Hk < 1 || rot < 0 || rot > D || rot % 16 ||
+      max_pos < 0)
+    return FP8SM_ERR_SHAPE;
+  if (T > kMaxTokens || Hq > kMaxHeads || Hk > kMaxHeads || max_pos > kMaxDim)
+    return FP8SM_ERR_RANGE;
+  const int64_t row = (int64_t)(Hq + Hk) * D;
+  if (ld_x < row || ld_y < row || (y == x && ld_y != ld_x)) return FP8SM_ERR_SHAPE;
+  if (ld_x % 8 || ld_y % 8) return FP8SM_ERR_ALIGN;
+  if (T == 0) return FP8SM_OK;
+  if (!x || !y || (rot > 0 && (!cos_sin || !pos)) || (q_weight == nullptr) != (k_weight == nullptr))
+    return FP8SM_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return FP8SM_ERR_ALIGN;
+  if (rot > 0 && (!aligned(cos_sin, 16) || !aligned(pos, 4))) return FP8SM_ERR_ALIGN;
+  fp8sm_status st = check_device();
+  if (st != FP8SM_OK) return st;
+  RopeArgs a;
+  a.x = x;
+  a.f16 = in == FP8SM_FP16;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.D = D;
+  a.ld_x = ld_x;
+  a.wq = q_weight;
+  a.wk = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.pos = pos;
+  a.max_pos = max_pos;
+  a.rot = rot;
+  a.interleaved = (flags & FP8SM_ROPE_INTERLEAVED) != 0;
+  a.y = y;
+  a.ld_y = ld_y;
+  return launched(launch_qk_norm_rope(a, stream));
+}
+
+fp8sm_status fp8sm_kv_cache_write(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                  fp8sm_dtype in, int64_t T, int64_t nseq, const int32_t* cu,
+                                  const int32_t* lens, const int32_t* table, int64_t ld_table,
+                                  int64_t max_blocks, int64_t num_blocks, int32_t Hkv, int32_t D,
+                                  int32_t block, uint8_t* k_codes, uint8_t* v_codes,
+                                  uint8_t* k_exp, uint8_t* v_exp, hipStream_t stream) {
+  if (in != FP8SM_BF16 && in != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
+  KvBatch kb;
+  KvCache c;
+  fp8sm_status st = kv_args(T, nseq, cu, lens, table, ld_table, max_blocks, k_codes, v_codes,
+                            k_exp, v_exp, num_blocks, Hkv, D, block, &kb, &c);
+  if (st != FP8SM_OK) return st;
+  if (ld_k < (int64_t)Hkv * D || ld_v < (int64_t)Hkv * D) return FP8SM_ERR_SHAPE;
+  if (ld_k % 8 || ld_v % 8) return FP8SM_ERR_ALIGN;
+  if (T == 0 || nseq == 0) return FP8SM_OK;
+  if (!k || !v) return FP8SM_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16)) return FP8SM_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8SM_OK) return st;
+  return launched(launch_kv_write(k, v, in == FP8SM_FP16, ld_k, ld_v, kb, c, stream));
+}
+
+fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
+                                 const uint8_t* k_exp, const uint8_t* v_exp, int64_t num_blocks,
+                                 int32_t Hkv, int32_t D, int32_t block, int64_t T, int64_t nseq,
+                                 const int32_t* cu, const int32_t* lens, const int32_t* table,
+                                 int64_t ld_table, int64_t max_blocks, fp8sm_dtype out, void* k,
+                                 int64_t ld_k, void* v, int64_t ld_v, hipStream_t stream) {
+  if (out != FP8SM_BF16 && out != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
+  KvBatch kb;
+  KvCache c;
+  fp8sm_status st = kv_args(T, nseq, cu, lens, table, ld_table, max_blocks, k_codes, v_codes,
+                            k_exp, v_exp, num_blocks, Hkv, D, block, &kb, &c);
+  if (st != FP8SM_OK) return st;
+  if ((k && ld_k < (int64_t)Hkv * D) || (v && ld_v < (int64_t)Hkv * D)) return FP8SM_ERR_SHAPE;
+  if ((k && ld_k % 8) || (v && ld_v % 8)) return FP8SM_ERR_ALIGN;
+  if (!aligned(k, 16) || !aligned(v, 16)) return FP8SM_ERR_ALIGN;
+  if (T == 0 || nseq == 0 || (!k && !v)) return FP8SM_OK;
+  st = check_device();
+  if (st != FP8SM_OK) return st;
+  return launched(launch_kv_read(kb, c, k, v, out == FP8SM_FP16, ld_k, ld_v, stream));
+}
+
+// Sizes that fp8sm_attention_cache's plan and workspace rest on.
+static bool attention_sizes(int64_t T, int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                            int64_t max_q, int64_t max_kv) {
+  return T > 0 && T <= kMaxTokens && nseq > 0 && nseq <= kMaxSeqs && Hkv >= 1 && Hkv <= kMaxHeads &&
+         Hq >= Hkv && Hq <= kMaxHeads && Hq % Hkv == 0 && T * Hq <= kMaxDim && (D == 64 || D == 128) &&
+         max_q >= 1 && max_kv >= 0;
+}
+
+static size_t attention_bytes(int64_t T, int32_t Hq, int32_t D, const AttnPlan& p) {
+  return p.nsplit > 1 ? (size_t)p.nsplit * T * Hq * (D + 2) * sizeof(float) : 0;
+}
+
+size_t fp8sm_attention_cache_workspace(int64_t T, int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                                       int64_t max_q, int64_t max_kv) {
+  if (!attention_sizes(T, nseq, Hq, Hkv, D, max_q, max_kv)) return 0;
+  return attention_bytes(T, Hq, D, plan_attention(T, nseq, Hq, Hkv, D, max_q, max_kv));
+}
+
+fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, int64_t T,
+                                   int64_t nseq, int32_t Hq, const int32_t* cu,
+                                   const int32_t* lens, const int32_t* table, int64_t ld_table,
+                                   int64_t max_blocks, const uint8_t* k_codes,
+                                   const uint8_t* v_codes, const uint8_t* k_exp,
+                                   const uint8_t* v_exp, int64_t num_blocks, int32_t Hkv,
+                                   int32_t D, int32_t block, int64_t max_q, int64_t max_kv,
+                                   float scale, uint32_t flags, int32_t window, void* o,
+                                   int64_t ld_o, float* lse, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+  if (in != FP8SM_BF16 && in != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
+  if (flags & ~FP8SM_ATTN_CAUSAL) return FP8SM_ERR_UNSUPPORTED;
+  AttnArgs a;
+  fp8sm_status st = kv_args(T, nseq, cu, lens, table, ld_table, max_blocks, k_codes, v_codes,
+                            k_exp, v_exp, num_blocks, Hkv, D, block, &a.kb, &a.c);
+  if (st != FP8SM_OK) return st;
+  if (Hq < 1 || Hq % Hkv || window < 0 || max_q < 1 || max_kv < 0) return FP8SM_ERR_SHAPE;
+  if (window > 0 && !(flags & FP8SM_ATTN_CAUSAL)) return FP8SM_ERR_UNSUPPORTED;
+  if (Hq > kMaxHeads || T * Hq > kMaxDim) return FP8SM_ERR_RANGE;
+  if (ld_q < (int64_t)Hq * D || ld_o < (int64_t)Hq * D) return FP8SM_ERR_SHAPE;
+  if (ld_q % 8 || ld_o % 8) return FP8SM_ERR_ALIGN;
+  if (T == 0 || nseq == 0) return FP8SM_OK;
+  if (!q || !o) return FP8SM_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return FP8SM_ERR_ALIGN;
+  const AttnPlan p = plan_attention(T, nseq, Hq, Hkv, D, max_q, max_kv);
+  const size_t need = attention_bytes(T, Hq, D, p);
+  if (need > 0 && !workspace) return FP8SM_ERR_NULL;
+  if (workspace_bytes < need) return FP8SM_ERR_SHAPE;
+  if (!aligned(workspace, 16)) return FP8SM_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8SM_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.ld_q = ld_q;
+  a.out = static_cast<uint16_t*>(o);
+  a.ld_o = ld_o;
+  a.lse = lse;
+  a.Hq = Hq;
+  a.G = Hq / Hkv;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.causal = (flags & FP8SM_ATTN_CAUSAL) != 0;
+  a.window = window;
+  a.nsplit = p.nsplit;
+  a.chunk = p.chunk;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + (need ? (size_t)p.nsplit * T * Hq * D : 0);
+  a.row_limit = p.row_limit;
+  return launched(launch_attention(a, in == FP8SM_FP16, p, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,691 @@
+// Attention of ragged 16-bit queries over the paged E4M3 cache (gfx950).
+//
+//   out[r] = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q_r . k_t)
+//
+// over the cached tokens t that row r sees: all of its sequence's, up to its
+// own position (causal), at most `window` of them.  One pass over the tokens
+// with a running maximum m and sum l in fp32 (in units of log2, so the
+// exponential is the hardware's 2^x).
+//
+// The query heads that share a key head are extra rows: row r of a sequence is
+// token r / G and head r % G of its G query heads, so both kernels read each
+// key and value once for all of them.  Scores are computed transposed,
+// S^T = K Q^T: a lane then holds scores of one row at consecutive tokens, which
+// is how the product O^T = V^T P^T wants its second operand, and V's cache
+// layout holds consecutive tokens of one channel, which is its first: neither
+// P nor V is moved between lanes.
+#include "kv_common.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace fp8sm {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Eight codes widened times a power of two, exactly unless the result leaves
+// the type's range.
+__device__ __forceinline__ bf16x8 widen_bf16(uint32_t d0, uint32_t d1, float s) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d0, s, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d0, s, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d1, s, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d1, s, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ f16x8 widen_f16(uint32_t d0, uint32_t d1, float s) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d0, s, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d0, s, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d1, s, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d1, s, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <bool F16>
+__device__ __forceinline__ uint16_t round16(float v) {
+  if constexpr (F16)
+    return __builtin_bit_cast(uint16_t, (_Float16)v);
+  else
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// Byte mask of a dword whose bytes are tokens t .. t + 3: those in [lo, hi).
+__device__ __forceinline__ uint32_t token_bytes(int t, int lo, int hi) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m |= (t + i >= lo && t + i < hi) ? 0xFFu << (8 * i) : 0u;
+  return m;
+}
+
+// The tokens that the rows [r0, r1) of a sequence see, [lo, hi), and the first
+// token of their split 0 (a multiple of 64).
+struct Span {
+  int lo, hi, start;
+  int chunk, splits;  // tokens of a split, splits in use
+};
+__device__ __forceinline__ Span row_span(const AttnArgs& a, const Seq& s, int r0, int r1) {
+  const int first = s.len - s.n + r0 / a.G, last = s.len - s.n + (r1 - 1) / a.G;
+  Span p;
+  p.hi = a.causal ? max(min(s.len, last + 1), 0) : s.len;
+  p.lo = a.window ? max(first - a.window + 1, 0) : 0;
+  p.start = p.lo & ~63;
+  // the plan's chunk, longer where the lengths go beyond what the plan was told
+  const int span = max(p.hi - p.start, 0);
+  p.chunk = max(a.chunk, ((span + a.nsplit - 1) / a.nsplit + 63) & ~63);
+  p.splits = (span + p.chunk - 1) / p.chunk;
+  return p;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: 16 QT rows of one sequence and key head per workgroup, the cached
+// tokens split over the grid and over the four wavefronts, 64 tokens a step.
+// Bound by the stream of codes from memory; every code goes straight from
+// memory to the registers of the lane that multiplies it.
+//
+// v_mfma_f32_16x16x32: lane l = 16 g + x holds row / column x and eight k
+// values of quarter g of both operands; of the result column x and rows
+// 4 g .. 4 g + 3.  Of a step's 64 tokens, key tile t (0..3) takes as its row m
+// token 16 (m / 4) + 4 t + m % 4, so that lane quarter g ends up with the
+// scores of the consecutive tokens 16 g .. 16 g + 15.
+template <bool F16, int D, int QT>
+__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
+  constexpr int NI = D / 64, DT = D / 16;
+  using op8 = std::conditional_t<F16, f16x8, bf16x8>;
+  const int lane = threadIdx.x & 63, x = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int bs = a.c.block_shift;
+  int64_t f0;
+  const int b = find_seq(a.kb, blockIdx.x, a.G, QT == 2 ? 5 : 4, 1, &f0);
+  const Seq s = load_seq(a.kb, b, bs);
+  const int rows = s.n * a.G;
+  const int r0 = (int)(blockIdx.x - f0) * (16 * QT);
+  if (r0 >= rows || rows > a.row_limit) return;
+  const int hk = blockIdx.y, split = blockIdx.z;
+  const Span sp = row_span(a, s, r0, min(r0 + 16 * QT, rows));
+  const int ns = sp.splits;
+  if (split >= max(ns, 1)) return;
+  const int t_begin = sp.start + split * sp.chunk;
+  const int t_end = min(sp.hi, t_begin + sp.chunk);  // ns == 0: no step
+
+  // rows of this lane: the query values, what they see, their running state
+  op8 qf[QT][2 * NI];
+  int see_lo[QT], see_hi[QT];
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    const int r = r0 + 16 * i + x;
+    const bool ok = r < rows;
+    const int tok = ok ? r / a.G : 0, p = s.len - s.n + tok;
+    see_hi[i] = ok ? (a.causal ? min(p + 1, s.len) : s.len) : 0;
+    see_lo[i] = ok && a.window ? max(p - a.window + 1, 0) : 0;
+    const uint16_t* q = a.q + (int64_t)(s.c0 + tok) * a.ld_q + (int64_t)(hk * a.G + (ok ? r - tok * a.G : 0)) * D;
+#pragma unroll
+    for (int k = 0; k < 2 * NI; ++k) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (ok) v = *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
+      qf[i][k] = __builtin_bit_cast(op8, v);
+    }
+  }
+  f32x4 o[QT][DT];
+  float m[QT], l[QT];
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[i][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  // no step needs a mask between these (every row sees all of it)
+  int all_lo = 0, all_hi = 0x7FFFFFFF;
+  {
+    const int first = s.len - s.n + r0 / a.G;
+    const int last = s.len - s.n + (min(r0 + 16 * QT, rows) - 1) / a.G;
+    if (a.causal) all_hi = first + 1;
+    all_hi = min(all_hi, s.len);
+    if (a.window) all_lo = last - a.window + 1;
+  }
+
+  const int32_t* table = a.kb.table + (int64_t)b * a.kb.ld_table;
+  const int in_mask = (1 << (bs - 4)) - 1;
+  struct Step {
+    uint4 k[4][NI], v[DT];
+    float ks, vs;  // the lane's key rows' and value tokens' scales
+    bool bad;      // the lane's value tokens have no block
+  };
+  const int last_run = max((t_end - 1) >> 4, 0);
+  auto fetch = [&](Step& st, int t0) {
+    const int kr = min((t0 >> 4) + (x >> 2), last_run), vr = min((t0 >> 4) + g, last_run);
+    int kp = table[kr >> (bs - 4)], vp = table[vr >> (bs - 4)];
+    st.bad = vp < 0 || vp >= a.c.num_blocks;
+    if (kp < 0 || kp >= a.c.num_blocks) kp = 0;
+    if (st.bad) vp = 0;
+    const int64_t kh = (int64_t)kp * a.c.heads + hk, vh = (int64_t)vp * a.c.heads + hk;
+    const uint8_t* kb = a.c.k + ((kh << bs) + ((kr & in_mask) << 4) + (x & 3)) * D + 16 * g;
+    const uint8_t* vb = a.c.v + ((vh << bs) + ((vr & in_mask) << 4)) * D + 16 * x;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) st.k[t][i] = load_stream16(kb + 4 * t * D + 64 * i);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) st.v[d] = load_stream16(vb + 256 * d);
+    st.ks = exp_byte_value(a.c.ke[F16 ? vh : kh]);
+    st.vs = exp_byte_value(a.c.ve[vh]);
+  };
+  auto compute = [&](Step& st, int t0) {
+    const bool partial = t0 + 64 > min(all_hi, t_end) || t0 < all_lo || __ballot(st.bad) != 0;
+    f32x4 sc[QT][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int i = 0; i < QT; ++i) sc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 2 * NI; ++k) {
+        const uint4 c = st.k[t][k >> 1];
+        const uint32_t c0 = (k & 1) ? c.z : c.x, c1 = (k & 1) ? c.w : c.y;
+        if constexpr (F16) {
+          const f16x8 kf = widen_f16(c0, c1, 1.0f);
+#pragma unroll
+          for (int i = 0; i < QT; ++i)
+            sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[i][k], sc[i][t], 0, 0, 0);
+        } else {
+          const bf16x8 kf = widen_bf16(c0, c1, st.ks);
+#pragma unroll
+          for (int i = 0; i < QT; ++i)
+            sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[i][k], sc[i][t], 0, 0, 0);
+        }
+      }
+    }
+    const float c = F16 ? a.scale_log2 * st.ks : a.scale_log2;
+    bf16x8 ph[QT][2], pl[QT][2];
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v = sc[i][t][k] * c;
+          if (partial) {
+            const int tok = t0 + 16 * g + 4 * t + k;
+            if (tok < see_lo[i] || tok >= min(see_hi[i], t_end) || st.bad) v = -INFINITY;
+          }
+          sc[i][t][k] = v;
+          mx = fmaxf(mx, v);
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      const float mn = fmaxf(m[i], mx);
+      const float ms = mn == -INFINITY ? 0.f : mn;
+      const float al = __builtin_amdgcn_exp2f(m[i] - ms);
+      m[i] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = __builtin_amdgcn_exp2f(sc[i][t][k] - ms);
+          sum += p;
+          const __bf16 hi = (__bf16)p;
+          ph[i][t >> 1][4 * (t & 1) + k] = hi;
+          if constexpr (F16) pl[i][t >> 1][4 * (t & 1) + k] = (__bf16)(p - (float)hi);
+        }
+      l[i] = __builtin_fmaf(l[i], al, sum);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][d][k] *= al;
+    }
+    if (partial) {  // what no row sees may hold anything, NaN codes too
+      const int t = t0 + 16 * g, lo = st.bad ? 0x7FFFFFFF : sp.lo;
+      uint32_t keep[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) keep[k] = token_bytes(t + 4 * k, lo, t_end);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        st.v[d].x &= keep[0];
+        st.v[d].y &= keep[1];
+        st.v[d].z &= keep[2];
+        st.v[d].w &= keep[3];
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c0 = h ? st.v[d].z : st.v[d].x, c1 = h ? st.v[d].w : st.v[d].y;
+        const bf16x8 vf = widen_bf16(c0, c1, st.vs);
+#pragma unroll
+        for (int i = 0; i < QT; ++i) {
+          o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph[i][h], o[i][d], 0, 0, 0);
+          if constexpr (F16)
+            o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl[i][h], o[i][d], 0, 0, 0);
+        }
+      }
+  };
+  {
+    Step st;
+    for (int t0 = t_begin + 64 * w; t0 < t_end; t0 += 256) {
+      fetch(st, t0);
+      compute(st, t0);
+    }
+  }
+
+  // join the four wavefronts
+  __shared__ float so[4][16 * QT][D + 4];
+  __shared__ float sm[4][16 * QT], sl[4][16 * QT];
+#pragma unroll
+  for (int i = 0; i < QT; ++i) {
+    l[i] += __shfl_xor(l[i], 16, 64);
+    l[i] += __shfl_xor(l[i], 32, 64);
+    if (g == 0) {
+      sm[w][16 * i + x] = m[i];
+      sl[w][16 * i + x] = l[i];
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      *reinterpret_cast<f32x4*>(&so[w][16 * i + x][16 * d + 4 * g]) = o[i][d];
+  }
+  __syncthreads();
+  constexpr int LPR = D / 8;  // lanes a row, eight channels each
+  for (int q = threadIdx.x; q < 16 * QT * LPR; q += 256) {
+    const int row = q / LPR, d = q % LPR * 8, r = r0 + row;
+    if (r >= rows) continue;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mm = fmaxf(mm, sm[k][row]);
+    const float ms = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, acc[8] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = __builtin_amdgcn_exp2f(sm[k][row] - ms);
+      ll = __builtin_fmaf(sl[k][row], f, ll);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(so[k][row][d + e], f, acc[e]);
+    }
+    const int tok = r / a.G, head = hk * a.G + (r - tok * a.G);
+    const int64_t t = s.c0 + tok;
+    if (ns <= 1) {
+      const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+      uint32_t u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        u[e] = (uint32_t)round16<F16>(acc[2 * e] * inv) | (uint32_t)round16<F16>(acc[2 * e + 1] * inv) << 16;
+      *reinterpret_cast<uint4*>(a.out + t * a.ld_o + head * D + d) = make_uint4(u[0], u[1], u[2], u[3]);
+      if (a.lse && d == 0) a.lse[t * a.Hq + head] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+    } else {
+      const int64_t at = ((int64_t)split * a.kb.T + t) * a.Hq + head;
+      float* po = a.part_o + at * D + d;
+      *reinterpret_cast<f32x4*>(po) = f32x4{acc[0], acc[1], acc[2], acc[3]};
+      *reinterpret_cast<f32x4*>(po + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};
+      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(mm, ll);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: 128 rows of one sequence and key head per workgroup, 32 a
+// wavefront, 64 tokens a step.  Codes are staged in LDS, two steps deep, and
+// widened by the wavefronts that multiply them.  Bound by the matrix
+// instructions and the softmax's vector arithmetic.
+//
+// v_mfma_f32_32x32x16: lane l = 32 h + x holds row / column x and eight k
+// values of half h of both operands; of the result column x and rows
+// 8 v + 4 h + i in register 4 v + i.  Of 32 tokens, row m of the key tile is
+// token 16 ((m >> 2) & 1) + 4 (m >> 3) + m % 4, so lane half h has the scores
+// of the consecutive tokens 16 h .. 16 h + 15 in its registers 0 .. 15.
+// P is rounded to fp16 (p <= 1: an error of 2^-12 of p, half a step) and V is
+// widened to fp16 relative to the largest value scale of the row tile's
+// blocks, so neither leaves fp16's range; the accumulator is fp32.
+constexpr int kPrefillRows = 128, kPrefillStep = 64;
+
+template <bool F16, int D>
+__global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
+  constexpr int DT = D / 32, NP = D / 32;      // channel tiles; 16-byte pieces of a lane's key row
+  constexpr int TILE = kPrefillStep * D;       // bytes of a step's keys or values
+  constexpr int CPT = TILE / 16 / 256;         // 16-byte pieces a thread stages of each
+  constexpr int CPR = D / 16;                  // pieces of a key row
+  using op8 = std::conditional_t<F16, f16x8, bf16x8>;
+  __shared__ __attribute__((aligned(16))) uint8_t lk[2][TILE], lv[2][TILE];
+  __shared__ float sks[2][4], svs[2][4];       // scales of a step's four runs of 16 tokens
+  __shared__ int sbad[2];
+  __shared__ int sref[4];
+  const int tid = threadIdx.x, lane = tid & 63, x = lane & 31, h = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int bs = a.c.block_shift;
+  int64_t f0;
+  const int b = find_seq(a.kb, blockIdx.x, a.G, 7, 1, &f0);
+  const Seq s = load_seq(a.kb, b, bs);
+  const int rows = s.n * a.G;
+  const int r0 = (int)(blockIdx.x - f0) * kPrefillRows;
+  if (r0 >= rows || rows <= a.row_limit) return;
+  const int hk = blockIdx.y, split = blockIdx.z;
+  const Span sp = row_span(a, s, r0, min(r0 + kPrefillRows, rows));
+  const int ns = sp.splits;
+  if (split >= max(ns, 1)) return;
+  const int t_begin = sp.start + split * sp.chunk;
+  const int t_end = min(sp.hi, t_begin + sp.chunk);
+  const int32_t* table = a.kb.table + (int64_t)b * a.kb.ld_table;
+  const int in_mask = (1 << (bs - 4)) - 1;
+
+  // the largest value exponent of the blocks in reach
+  int eref = 0;
+  if (t_begin < t_end) {
+    for (int p = (t_begin >> bs) + tid; p <= (t_end - 1) >> bs; p += 256) {
+      const int page = table[p];
+      if (page >= 0 && page < a.c.num_blocks) eref = max(eref, (int)a.c.ve[(int64_t)page * a.c.heads + hk]);
+    }
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) eref = max(eref, __shfl_xor(eref, k, 64));
+    if (lane == 0) sref[w] = eref;
+    __syncthreads();
+    eref = max(max(sref[0], sref[1]), max(sref[2], sref[3]));
+  }
+
+  const int r = r0 + 32 * w + x;
+  const bool ok = r < rows;
+  const int tok = ok ? r / a.G : 0, head = hk * a.G + (ok ? r - tok * a.G : 0);
+  const int pos = s.len - s.n + tok;
+  const int see_hi = ok ? (a.causal ? min(pos + 1, s.len) : s.len) : 0;
+  const int see_lo = ok && a.window ? max(pos - a.window + 1, 0) : 0;
+  op8 qf[2 * NP];
+  {
+    const uint16_t* q = a.q + (int64_t)(s.c0 + tok) * a.ld_q + (int64_t)head * D;
+#pragma unroll
+    for (int k = 0; k < 2 * NP; ++k) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (ok) v = *reinterpret_cast<const uint4*>(q + 32 * (k >> 1) + 16 * h + 8 * (k & 1));
+      qf[k] = __builtin_bit_cast(op8, v);
+    }
+  }
+  // what this wavefront's rows see: nothing outside [w_lo, w_hi), all of it
+  // inside [all_lo, all_hi)
+  int w_lo = 0, w_hi = 0, all_lo = 0, all_hi = 0;
+  {
+    const int a0 = r0 + 32 * w, a1 = min(a0 + 32, rows);
+    if (a0 < a1) {
+      const int first = s.len - s.n + a0 / a.G, last = s.len - s.n + (a1 - 1) / a.G;
+      w_hi = a.causal ? max(min(s.len, last + 1), 0) : s.len;
+      all_hi = a.causal ? min(s.len, first + 1) : s.len;
+      w_lo = a.window ? max(first - a.window + 1, 0) : 0;
+      all_lo = a.window ? last - a.window + 1 : 0;
+    }
+  }
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[d][k] = 0.f;
+  float m = -INFINITY, l = 0.f;
+
+  // staging: thread t copies pieces t + 256 j
+  uint4 rk[CPT], rv[CPT];
+  float rks = 0.f, rvs = 0.f;
+  int rbad = 0;
+  const int last_run = max((t_end - 1) >> 4, 0);
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+      const int c = tid + 256 * j;
+      {
+        const int row = c / CPR, cc = c % CPR;
+        const int key = D == 128 ? ((row & 3) | ((row >> 4) & 1) << 2) : (((row >> 1) & 1) | ((row >> 4) & 1) << 1);
+        const int run = min((t0 + row) >> 4, last_run);
+        int page = table[run >> (bs - 4)];
+        if (page < 0 || page >= a.c.num_blocks) page = 0;
+        const int64_t ph = (int64_t)page * a.c.heads + hk;
+        rk[j] = *reinterpret_cast<const uint4*>(
+            a.c.k + ((ph << bs) + ((run & in_mask) << 4) + (row & 15)) * D + 16 * (cc ^ key));
+      }
+      {
+        const int sub = c / D, d = c % D;
+        const int run = min((t0 >> 4) + sub, last_run);
+        int page = table[run >> (bs - 4)];
+        const bool bad = page < 0 || page >= a.c.num_blocks;
+        if (bad) page = 0;
+        const int64_t ph = (int64_t)page * a.c.heads + hk;
+        uint4 v = *reinterpret_cast<const uint4*>(a.c.v + ((ph << bs) + ((run & in_mask) << 4)) * D + 16 * d);
+        const int t = t0 + 16 * sub;
+        if (bad || t < sp.lo || t + 16 > t_end) {  // what no row sees may hold anything
+          const int lo = bad ? 0x7FFFFFFF : sp.lo;
+          v.x &= token_bytes(t, lo, t_end);
+          v.y &= token_bytes(t + 4, lo, t_end);
+          v.z &= token_bytes(t + 8, lo, t_end);
+          v.w &= token_bytes(t + 12, lo, t_end);
+        }
+        rv[j] = v;
+      }
+    }
+    if (tid < 64) {
+      const int run = min((t0 >> 4) + (tid & 3), last_run);
+      int page = table[run >> (bs - 4)];
+      const bool bad = page < 0 || page >= a.c.num_blocks;
+      if (bad) page = 0;
+      const int64_t ph = (int64_t)page * a.c.heads + hk;
+      rks = exp_byte_value(a.c.ke[ph]);
+      rvs = bad ? 1.f : pow2f(max((int)a.c.ve[ph] - eref, -126));
+      rbad = (int)(__ballot(bad) & 15);
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int j = 0; j < CPT; ++j) {
+      *reinterpret_cast<uint4*>(&lk[buf][(tid + 256 * j) * 16]) = rk[j];
+      *reinterpret_cast<uint4*>(&lv[buf][(tid + 256 * j) * 16]) = rv[j];
+    }
+    if (tid < 4) {
+      sks[buf][tid] = rks;
+      svs[buf][tid] = rvs;
+    }
+    if (tid == 0) sbad[buf] = rbad;
+  };
+  // the lane's key row of 32 tokens, and its pieces' swizzled places
+  const int krow = 16 * ((x >> 2) & 1) + 4 * (x >> 3) + (x & 3);
+  const int kkey = D == 128 ? ((krow & 3) | ((krow >> 4) & 1) << 2) : (((krow >> 1) & 1) | ((krow >> 4) & 1) << 1);
+
+  auto compute = [&](int buf, int t0) {
+    const int bad = sbad[buf];
+    const bool partial = t0 + kPrefillStep > all_hi || t0 < all_lo || t0 + kPrefillStep > t_end || bad;
+    f32x16 sc[2];
+#pragma unroll
+    for (int grp = 0; grp < 2; ++grp) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sc[grp][k] = 0.f;
+      const float ks = F16 ? 1.0f : sks[buf][2 * grp + (krow >> 4)];
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        const uint4 c = *reinterpret_cast<const uint4*>(
+            &lk[buf][(32 * grp + krow) * D + 16 * ((2 * u + h) ^ kkey)]);
+        if constexpr (F16) {
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, ks), qf[2 * u], sc[grp], 0, 0, 0);
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, ks), qf[2 * u + 1], sc[grp], 0, 0, 0);
+        } else {
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16(c.x, c.y, ks), qf[2 * u], sc[grp], 0, 0, 0);
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16(c.z, c.w, ks), qf[2 * u + 1], sc[grp], 0, 0, 0);
+        }
+      }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int grp = 0; grp < 2; ++grp) {
+      const float c = F16 ? a.scale_log2 * sks[buf][2 * grp + h] : a.scale_log2;
+      const bool gone = (bad >> (2 * grp + h)) & 1;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float v = sc[grp][k] * c;
+        if (partial) {
+          const int t = t0 + 32 * grp + 16 * h + k;
+          if (t < see_lo || t >= min(see_hi, t_end) || gone) v = -INFINITY;
+        }
+        sc[grp][k] = v;
+        mx = fmaxf(mx, v);
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const float mn = fmaxf(m, mx);
+    const float ms = mn == -INFINITY ? 0.f : mn;
+    const float al = __builtin_amdgcn_exp2f(m - ms);
+    m = mn;
+    float sum = 0.f;
+    f16x8 p[4];
+#pragma unroll
+    for (int grp = 0; grp < 2; ++grp)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float e = __builtin_amdgcn_exp2f(sc[grp][k] - ms);
+        sum += e;
+        p[2 * grp + (k >> 3)][k & 7] = (_Float16)e;
+      }
+    l = __builtin_fmaf(l, al, sum);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[d][k] *= al;
+#pragma unroll
+    for (int grp = 0; grp < 2; ++grp) {
+      const float vs = svs[buf][2 * grp + h];
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const uint4 c = *reinterpret_cast<const uint4*>(&lv[buf][((2 * grp + h) * D + 32 * d + x) * 16]);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, vs), p[2 * grp], o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, vs), p[2 * grp + 1], o[d], 0, 0, 0);
+      }
+    }
+  };
+
+  if (t_begin < t_end) {
+    load(t_begin);
+    store(0);
+    int buf = 0;
+    for (int t0 = t_begin; t0 < t_end; t0 += kPrefillStep, buf ^= 1) {
+      __syncthreads();  // the step's pieces are there; the other buffer is read no more
+      const bool more = t0 + kPrefillStep < t_end;
+      if (more) load(t0 + kPrefillStep);
+      if (t0 < w_hi && t0 + kPrefillStep > w_lo) compute(buf, t0);
+      if (more) store(buf ^ 1);
+    }
+  }
+  l += __shfl_xor(l, 32, 64);
+  if (!ok) return;
+  const int64_t t = s.c0 + tok;
+  const float vref = exp_byte_value(eref);
+  if (ns <= 1) {
+    const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+    uint16_t* dst = a.out + t * a.ld_o + head * D;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        uint32_t u[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          u[e] = (uint32_t)round16<F16>(o[d][4 * v + 2 * e] * inv * vref) |
+                 (uint32_t)round16<F16>(o[d][4 * v + 2 * e + 1] * inv * vref) << 16;
+        *reinterpret_cast<uint2*>(dst + 32 * d + 8 * v + 4 * h) = make_uint2(u[0], u[1]);
+      }
+    if (a.lse && h == 0) a.lse[t * a.Hq + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+  } else {
+    const int64_t at = ((int64_t)split * a.kb.T + t) * a.Hq + head;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        *reinterpret_cast<f32x4*>(a.part_o + at * D + 32 * d + 8 * v + 4 * h) =
+            f32x4{o[d][4 * v] * vref, o[d][4 * v + 1] * vref, o[d][4 * v + 2] * vref, o[d][4 * v + 3] * vref};
+    if (h == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, l);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the splits of a row: one wavefront per row, splits in ascending order.
+template <bool F16, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_rows) {
+  constexpr int E = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (id >= (int64_t)a.kb.T * a.Hq) return;
+  const int t = (int)(id / a.Hq), head = (int)(id - (int64_t)t * a.Hq);
+  int64_t f0;
+  const int b = find_seq(a.kb, t, 1, 0, 0, &f0);
+  const Seq s = load_seq(a.kb, b, a.c.block_shift);
+  if (t < s.c0 || t >= s.c0 + s.n) return;  // no sequence's row
+  const int rows = s.n * a.G;
+  const int tile = rows > a.row_limit ? kPrefillRows : decode_rows;
+  const int r = (t - s.c0) * a.G + head % a.G, r0 = r / tile * tile;
+  const int ns = row_span(a, s, r0, min(r0 + tile, rows)).splits;
+  if (ns <= 1) return;  // written already
+  const int64_t step = (int64_t)a.kb.T * a.Hq;
+  float mm = -INFINITY;
+  for (int i = 0; i < ns; ++i) mm = fmaxf(mm, a.part_ml[2 * (id + i * step)]);
+  const float ms = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f, acc[E] = {};
+  for (int i = 0; i < ns; ++i) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (id + i * step));
+    const float f = __builtin_amdgcn_exp2f(ml.x - ms);
+    ll = __builtin_fmaf(ml.y, f, ll);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(a.part_o[(id + i * step) * D + lane * E + e], f, acc[e]);
+  }
+  const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) a.out[(int64_t)t * a.ld_o + head * D + lane * E + e] = round16<F16>(acc[e] * inv);
+  if (a.lse && lane == 0) a.lse[id] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// The plan, from sizes alone (the lengths are on the device).
+AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv) {
+  (void)D;
+  const int64_t G = Hq / Hkv;
+  AttnPlan p;
+  max_q = std::min(max_q, T);
+  max_kv = std::min<int64_t>(max_kv, 1 << 30);
+  const int64_t max_rows = max_q * G;
+  p.prefill = max_rows > 64;
+  // with the prefill kernel the decode kernel takes the short sequences of a
+  // mixed batch only
+  p.decode_tiles = std::min<int64_t>(max_rows, 64) <= 16 && !p.prefill ? 1 : 2;
+  if (!p.prefill) p.row_limit = 0x7FFFFFFF;
+  else if (B * max_q == T) p.row_limit = p.decode_tiles = 0;  // no short ones, by what we are told
+  else p.row_limit = 64;
+  const int64_t tile = p.prefill ? kPrefillRows : 16 * p.decode_tiles;
+  const int64_t tiles = std::max<int64_t>(1, std::max<int64_t>(T * G / tile, std::min(B, T))) * Hkv;
+  const int64_t want = p.prefill ? 512 : 1024;
+  const int64_t unit = p.prefill ? 512 : 256;
+  int64_t ns = std::max<int64_t>(1, want / tiles);
+  int64_t chunk = (max_kv + ns - 1) / ns;
+  chunk = std::max<int64_t>(unit, (chunk + unit - 1) / unit * unit);
+  p.chunk = (int)chunk;
+  p.nsplit = (int)std::max<int64_t>(1, (max_kv + chunk - 1) / chunk);
+  return p;
+}
+
+template <bool F16, int D>
+static void attn_launch(AttnArgs a, const AttnPlan& p, hipStream_t s) {
+  const int64_t R = (int64_t)a.kb.T * a.G;
+  if (p.prefill) {
+    const dim3 grid((uint32_t)(R / kPrefillRows + a.kb.B), a.c.heads, p.nsplit);
+    attn_prefill_kernel<F16, D><<<grid, 256, 0, s>>>(a);
+  }
+  if (p.decode_tiles == 1) {
+    const dim3 grid((uint32_t)(R / 16 + a.kb.B), a.c.heads, p.nsplit);
+    attn_decode_kernel<F16, D, 1><<<grid, 256, 0, s>>>(a);
+  } else if (p.decode_tiles == 2) {
+    const dim3 grid((uint32_t)(R / 32 + a.kb.B), a.c.heads, p.nsplit);
+    attn_decode_kernel<F16, D, 2><<<grid, 256, 0, s>>>(a);
+  }
+  if (p.nsplit > 1)
+    attn_join_kernel<F16, D><<<(uint32_t)(((int64_t)a.kb.T * a.Hq + 3) / 4), 256, 0, s>>>(a, 16 * p.decode_tiles);
+}
+
+hipError_t launch_attention(const AttnArgs& a, bool f16, const AttnPlan& p, hipStream_t s) {
+  if (a.c.D == 64)
+    f16 ? attn_launch<true, 64>(a, p, s) : attn_launch<false, 64>(a, p, s);
+  else
+    f16 ? attn_launch<true, 128>(a, p, s) : attn_launch<false, 128>(a, p, s);
+  return hipGetLastError();
+}
+
+}  // namespace fp8sm

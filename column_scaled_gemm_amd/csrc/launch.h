@@ -1,6 +1,6 @@
 // Internal launcher interface between the C-ABI layer (api.cpp) and the
-// kernels (quant.hip, gemm.hip).  No device code here; the two batch structs
-// are also passed to kernels by value.
+// kernels (*.hip).  No device code here; the batch and cache
+// structs are also passed to kernels by value.
 #pragma once
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
@@ -123,5 +123,73 @@ hipError_t launch_rate_probe(int widen, int blocks, int waves_per_block, int ite
                              hipStream_t s);
 hipError_t launch_fill_k0(uint16_t* C, int64_t ldc, int64_t M, int64_t N, const void* bias,
                           hipStream_t s, const GemmBatch& bt = GemmBatch{1, 0, 0, 0, 0, 0, nullptr});
+
+// A ragged batch over a paged cache: sequence b's rows of the token arrays are
+// cu[b] .. cu[b+1]-1, its cached length (those tokens included) lens[b], its
+// block numbers table[b * ld_table ..].  Device arrays; the kernels clamp them.
+struct KvBatch {
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* table;
+  int64_t ld_table;
+  int max_blocks;
+  int T, B;
+};
+
+// The cache: K codes [blocks][heads][block][D], V codes
+// [blocks][heads][block / 16][D][16], biased exponents [blocks][heads].
+struct KvCache {
+  uint8_t *k, *v, *ke, *ve;
+  int num_blocks, heads, D, block_shift;
+};
+
+struct RopeArgs {
+  const void* x;
+  bool f16;
+  int64_t T;
+  int Hq, Hk, D;
+  int64_t ld_x;
+  const void *wq, *wk;  // both or neither
+  float eps;
+  const float* cos_sin;
+  const int32_t* pos;
+  int64_t max_pos;
+  int rot;
+  bool interleaved;
+  void* y;
+  int64_t ld_y;
+};
+hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t s);
+hipError_t launch_kv_write(const void* k, const void* v, bool f16, int64_t ld_k, int64_t ld_v,
+                           const KvBatch& kb, const KvCache& c, hipStream_t s);
+hipError_t launch_kv_read(const KvBatch& kb, const KvCache& c, void* k, void* v, bool f16,
+                          int64_t ld_k, int64_t ld_v, hipStream_t s);
+
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t ld_q;
+  uint16_t* out;
+  int64_t ld_o;
+  float* lse;  // [T][Hq] or nullptr
+  KvBatch kb;
+  KvCache c;
+  int Hq, G;
+  float scale_log2;  // softmax scale * log2(e)
+  int causal, window;
+  // split over the cached tokens: a row tile's split s covers `chunk` tokens;
+  // part_o [split][T][Hq][D], part_ml [split][T][Hq] hold unjoined results
+  int nsplit, chunk;
+  float* part_o;
+  float* part_ml;
+  int row_limit;  // sequences of at most this many rows (tokens x G) are the decode kernel's
+};
+struct AttnPlan {
+  int decode_tiles;  // 16-row tiles of a decode workgroup, 0: the decode kernel is not launched
+  bool prefill;      // the prefill kernel is launched
+  int row_limit;
+  int nsplit, chunk;
+};
+AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv);
+hipError_t launch_attention(const AttnArgs& a, bool f16, const AttnPlan& p, hipStream_t s);
 
 }  // namespace fp8sm

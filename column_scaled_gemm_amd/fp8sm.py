@@ -8,6 +8,7 @@ load, every call raises -- there is no fallback.
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -24,6 +25,8 @@ LAYOUT_ROW_MAJOR, LAYOUT_MN_MAJOR = 0, 1
 KIND_TENSOR, KIND_ROW, KIND_COL = 0, 1, 2
 KIND_GROUP128_UE8M0, KIND_GROUP128_FP32, KIND_BLOCK128 = 3, 4, 5
 FUSE_SILU_MUL = 1
+ROPE_INTERLEAVED = 1
+ATTN_CAUSAL = 1
 
 # Every symbol include/fp8sm.h declares, with (restype, argtypes).
 _i64, _i32, _u32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p
@@ -47,6 +50,17 @@ SIGNATURES = {
     "fp8sm_scaled_mm_batched": (_int, [_i64, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64,
                                        _i64, _i64, _i64, _int, _p, _i64, _int, _p, _i64, _p, _int,
                                        _p]),
+    "fp8sm_qk_norm_rope": (_int, [_p, _int, _i64, _i32, _i32, _i32, _i64, _p, _p, ctypes.c_float, _p,
+                                  _i64, _p, _i32, _u32, _p, _i64, _p]),
+    "fp8sm_kv_cache_write": (_int, [_p, _i64, _p, _i64, _int, _i64, _i64, _p, _p, _p, _i64, _i64,
+                                    _i64, _i32, _i32, _i32, _p, _p, _p, _p, _p]),
+    "fp8sm_kv_cache_read": (_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _i64, _i64, _p, _p, _p,
+                                   _i64, _i64, _int, _p, _i64, _p, _i64, _p]),
+    "fp8sm_attention_cache": (_int, [_p, _i64, _int, _i64, _i64, _i32, _p, _p, _p, _i64, _i64, _p,
+                                     _p, _p, _p, _i64, _i32, _i32, _i32, _i64, _i64,
+                                     ctypes.c_float, _u32, _i32, _p, _i64, _p, _p,
+                                     ctypes.c_size_t, _p]),
+    "fp8sm_attention_cache_workspace": (ctypes.c_size_t, [_i64, _i64, _i32, _i32, _i32, _i64, _i64]),
     "fp8sm_scale_bytes": (ctypes.c_size_t, [_int, _int, _i64, _i64, _i32]),
     "fp8sm_status_str": (ctypes.c_char_p, [_int]),
     "fp8sm_force_variant": (_int, [_int]),
@@ -602,3 +616,203 @@ def quant_group_scatter(x, dst, R, fmt=SCALE_UE8M0_BYTE, layout=LAYOUT_MN_MAJOR,
                                            _ptr(scales), _stream(stream))
     _check(st, "fp8sm_quant_group_scatter")
     return q, scales
+
+
+# ---------------------------------------------------------------- QKV projection to attention
+
+def _head_rows(t, heads, head_dim, what):
+    """A [T, heads, D] view with the heads side by side, or a [T, heads * D]
+    matrix -> (rows, row stride in elements)."""
+    sh = t.shape
+    if len(sh) == 3:
+        ok = sh[1] == heads and sh[2] == head_dim and (heads == 1 or t.stride(1) == head_dim)
+    else:
+        ok = len(sh) == 2 and sh[1] == heads * head_dim
+    if not ok or t.stride(-1) != 1:
+        raise ValueError(f"{what}: needs [T, {heads}, {head_dim}] or [T, {heads * head_dim}] with each "
+                         f"row's heads side by side, got {tuple(sh)}, strides {t.stride()}")
+    return sh[0], (t.stride(0) if sh[0] > 1 else heads * head_dim)
+
+
+def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_weight=None,
+                 k_weight=None, eps=1e-6, interleaved=False, out=None, stream=None):
+    """x [T, >= (q_heads + k_heads) * head_dim] bf16/fp16, rows of query heads
+    then key heads (what follows is not read) -> the same heads, each RMS-normed
+    with q_weight / k_weight [head_dim] (both or neither) and rotated by the row
+    positions[t] (device int32 [T]) of cos_sin (device fp32 [positions, rot]: rot/2
+    cosines, then sines; None: no rotation).  Rows at positions outside the table
+    are padding and left as `out` held them.  out=x works in place."""
+    T = x.shape[0]
+    row = (q_heads + k_heads) * head_dim
+    _unit_last(x, "x")
+    _holds(x, (T, row), "x")
+    if out is None:
+        out = torch.empty((T, row), dtype=x.dtype, device=x.device)
+    else:
+        _unit_last(out, "out")
+        _holds(out, (T, row), "out", x.dtype)
+    rot = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin: needs [positions, rot]")
+        max_pos, rot = cos_sin.shape
+        _holds_bytes(cos_sin, 0, "cos_sin", torch.float32)
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+        _holds_bytes(positions, 4 * T, "positions", torch.int32)
+    for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _holds_bytes(t, 2 * head_dim, what, x.dtype)
+    st = _load().fp8sm_qk_norm_rope(_ptr(x), _dtype_code(x), T, q_heads, k_heads, head_dim,
+                                    _row_ld(x), _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin),
+                                    max_pos, _ptr(positions), rot,
+                                    ROPE_INTERLEAVED if interleaved else 0, _ptr(out),
+                                    _row_ld(out), _stream(stream))
+    _check(st, "fp8sm_qk_norm_rope")
+    return out
+
+
+def _row_ld(t):
+    """Row stride of a matrix, its width rounded up to 8 where it has one row at most."""
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+class KVCache(NamedTuple):
+    """A paged E4M3 key/value cache: k [blocks, heads, block, D] and v [blocks,
+    heads, block/16, D, 16] codes (uint8), k_exp and v_exp [blocks, heads] biased
+    exponents (uint8).  A value is code * 2^(exponent - 127)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+
+
+def kv_cache_empty(num_blocks, heads, head_dim, block, device="cuda"):
+    """A cache whose blocks hold no tokens yet."""
+    def e(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device=device)
+    return KVCache(e(num_blocks, heads, block, head_dim),
+                   e(num_blocks, heads, block // 16, head_dim, 16),
+                   e(num_blocks, heads), e(num_blocks, heads))
+
+
+def _cache_args(cache):
+    """(blocks, heads, D, block) of a cache whose four tensors agree."""
+    k, v, ke, ve = cache
+    if k.dim() != 4:
+        raise ValueError(f"cache.k: needs [blocks, heads, block, D], got {tuple(k.shape)}")
+    P, H, block, D = k.shape
+    if v.shape != (P, H, block // 16, D, 16) or ke.shape != (P, H) or ve.shape != (P, H):
+        raise ValueError(f"cache: v {tuple(v.shape)}, k_exp {tuple(ke.shape)}, v_exp {tuple(ve.shape)} "
+                         f"do not go with k {tuple(k.shape)}")
+    for t in cache:
+        if t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError("cache: needs contiguous uint8 tensors")
+    return P, H, D, block
+
+
+def _batch_args(cu, lens, table):
+    """(sequences, table row stride, blocks a sequence) of a ragged batch."""
+    B = lens.shape[0]
+    if cu.dtype != torch.int32 or lens.dtype != torch.int32 or table.dtype != torch.int32:
+        raise TypeError("cu, lens and table must be int32")
+    if cu.dim() != 1 or lens.dim() != 1 or cu.shape[0] != B + 1 or table.dim() != 2 or \
+            table.shape[0] != B:
+        raise ValueError(f"cu {tuple(cu.shape)}, lens {tuple(lens.shape)}, table {tuple(table.shape)}: "
+                         "need [B + 1], [B], [B, blocks]")
+    if not cu.is_contiguous() or not lens.is_contiguous() or \
+            (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("cu, lens and the rows of table must be contiguous")
+    n = table.shape[1]
+    return B, (table.stride(0) if B > 1 else n), n
+
+
+def kv_cache_write(k, v, cache, cu, lens, table, stream=None):
+    """Quantise new keys and values k, v [T, heads, D] (or [T, heads * D]; bf16 or
+    fp16, any row stride) into the cache.  Sequence b's rows are cu[b] ..
+    cu[b+1]-1 and its lens[b] cached tokens, these included, lie in the blocks
+    table[b] (all device int32).  -> cache, written in place."""
+    P, H, D, block = _cache_args(cache)
+    B, ld_table, n = _batch_args(cu, lens, table)
+    T, ld_k = _head_rows(k, H, D, "k")
+    Tv, ld_v = _head_rows(v, H, D, "v")
+    if Tv != T or v.dtype != k.dtype:
+        raise ValueError("k and v must have the same rows and dtype")
+    st = _load().fp8sm_kv_cache_write(
+        _ptr(k), ld_k, _ptr(v), ld_v, _dtype_code(k), T, B, _ptr(cu), _ptr(lens), _ptr(table),
+        ld_table, n, P, H, D, block, _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
+        _ptr(cache[3]), _stream(stream))
+    _check(st, "fp8sm_kv_cache_write")
+    return cache
+
+
+def kv_cache_read(cache, cu, lens, table, total, dtype=torch.bfloat16, k=None, v=None,
+                  stream=None):
+    """The last cu[b+1] - cu[b] cached tokens of every sequence, widened ->
+    (k, v), each [total, heads, D]; total >= cu[-1], rows past it unwritten."""
+    P, H, D, block = _cache_args(cache)
+    B, ld_table, n = _batch_args(cu, lens, table)
+    if k is None:
+        k = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
+    if v is None:
+        v = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
+    Tk, ld_k = _head_rows(k, H, D, "k")
+    Tv, ld_v = _head_rows(v, H, D, "v")
+    if Tk < total or Tv < total or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError(f"k and v need {total} rows of {dtype}")
+    st = _load().fp8sm_kv_cache_read(
+        _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]), _ptr(cache[3]), P, H, D, block, total, B,
+        _ptr(cu), _ptr(lens), _ptr(table), ld_table, n, _dtype_code(k), _ptr(k), ld_k, _ptr(v),
+        ld_v, _stream(stream))
+    _check(st, "fp8sm_kv_cache_read")
+    return k, v
+
+
+def attention_cache_workspace(T, nseq, q_heads, kv_heads, head_dim, max_q, max_kv):
+    """Bytes of workspace of an attention_cache call of these sizes."""
+    return _load().fp8sm_attention_cache_workspace(T, nseq, q_heads, kv_heads, head_dim, max_q,
+                                                   max_kv)
+
+
+def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, causal=True,
+                    window=0, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """q [T, Hq, D] bf16/fp16 (any row stride): attention of each sequence's rows,
+    its last tokens, over its lens[b] cached tokens -> out [T, Hq, D], or (out,
+    lse fp32 [T, Hq]) with return_lse.  Hq is a multiple of the cache's heads;
+    scale defaults to D^-1/2.  max_q >= every cu[b+1] - cu[b] and max_kv >= every
+    lens[b] (default: the table's reach) only steer the choice of kernels.
+    workspace: uint8, attention_cache_workspace bytes; allocated here if None."""
+    P, H, D, block = _cache_args(cache)
+    B, ld_table, n = _batch_args(cu, lens, table)
+    if q.dim() != 3:
+        raise ValueError("q: needs [T, heads, D]")
+    Hq = q.shape[1]
+    T, ld_q = _head_rows(q, Hq, D, "q")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        ld_o = Hq * D
+    else:
+        To, ld_o = _head_rows(out, Hq, D, "out")
+        if To < T or out.dtype != q.dtype:
+            raise ValueError(f"out: needs {T} rows of {q.dtype}")
+    if lse is not None:
+        _holds_bytes(lse, 4 * T * Hq, "lse", torch.float32)
+    elif return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    if max_kv is None:
+        max_kv = n * block
+    L = _load()
+    need = L.fp8sm_attention_cache_workspace(T, B, Hq, H, D, max_q, max_kv)
+    if workspace is not None:
+        _holds_bytes(workspace, need, "workspace", torch.uint8)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    st = L.fp8sm_attention_cache(
+        _ptr(q), ld_q, _dtype_code(q), T, B, Hq, _ptr(cu), _ptr(lens), _ptr(table), ld_table, n,
+        _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]), _ptr(cache[3]), P, H, D, block, max_q,
+        max_kv, D ** -0.5 if scale is None else scale, ATTN_CAUSAL if causal else 0, window,
+        _ptr(out), ld_o, _ptr(lse), _ptr(workspace), need, _stream(stream))
+    _check(st, "fp8sm_attention_cache")
+    return (out, lse) if return_lse else out

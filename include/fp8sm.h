@@ -308,6 +308,141 @@ fp8sm_status fp8sm_scales_to_channelwise(const float* scales, const int64_t* wid
 fp8sm_status fp8sm_silu_mul_f32(const void* x, fp8sm_dtype in, int64_t M, int64_t K_out,
                                 int64_t ld_x, float* y, int64_t ld_y, hipStream_t stream);
 
+/*
+ * ---- From the QKV projection to attention ----
+ *
+ * A ragged batch of nseq sequences lies in token-major arrays of T rows:
+ * sequence b has the rows cu[b] .. cu[b+1]-1 (device int32 [nseq+1],
+ * non-decreasing), n_b of them, and lens[b] (device int32 [nseq]) cached
+ * tokens, counted WITH those n_b, which are the last ones: row cu[b] + i is at
+ * position lens[b] - n_b + i.  Its blocks are table[b * ld_table + j] (device
+ * int32, max_blocks a sequence), block j holding positions j * block ..
+ * j * block + block - 1.  The arrays are read on the device, so the calls
+ * need no host sync and can be captured in a graph and replayed with other
+ * lengths.  They are clamped there: rows lie in [0, T), lengths in [0,
+ * max_blocks * block]; a block number outside [0, num_blocks) names no block
+ * (its tokens are not written, read as zeros and are seen by no query), and a
+ * position below 0 (lens[b] < n_b) no token.  Rows of no sequence are left as
+ * they were.
+ *
+ * The cache is four device arrays, owned by the caller:
+ *   k_codes  uint8 E4M3FN [num_blocks][Hkv][block][D]
+ *   v_codes  uint8 E4M3FN [num_blocks][Hkv][block/16][D][16]  (16 tokens of a
+ *            channel side by side)
+ *   k_exp, v_exp  uint8 [num_blocks][Hkv]: one power-of-two scale per block of
+ *            tokens and head, as the biased exponent of FP8SM_SCALE_UE8M0_BYTE:
+ *            value = code * 2^(byte - 127), byte 0..254.
+ * Codes 16-byte aligned.  block is 16, 32, 64 or 128; D is 64 or 128.
+ * Common errors: T, nseq < 0, heads < 1, num_blocks < 1, max_blocks < 1, ld
+ * below a row's length, ld_table < max_blocks -> ERR_SHAPE; D or block not
+ * listed -> ERR_UNSUPPORTED; T > 2^24, nseq > 2^20, heads > 1024, num_blocks >
+ * 2^31 - 1, max_blocks * block > 2^30 -> ERR_RANGE; alignment -> ERR_ALIGN.
+ * T == 0 or nseq == 0 launches nothing.
+ */
+
+/*
+ * RMS norm of every query and key head and the rotation by position, in one
+ * pass: for each head x of D values, in fp32 with one rounding at the end,
+ *   y = x * rsqrt(mean(x^2) + eps) * w       (w: q_weight or k_weight)
+ * and for each pair (a, b) of y's first `rot` values, with c, s from the row
+ * pos[t] of the table,
+ *   (a, b) -> (a c - b s, b c + a s).
+ *   x     device bf16/fp16 [T][ld_x]: Hq query heads, then Hk key heads, as a
+ *         QKV product's rows begin; what follows in a row is not touched.
+ *   q_weight, k_weight  device [D] of the same type, both or neither (no norm).
+ *   cos_sin  device fp32 [max_pos][rot]: rot/2 cosines, then rot/2 sines.
+ *   pos   device int32 [T].  A row whose position is outside [0, max_pos) is
+ *         padding: its row of y is not written.
+ *   rot   0 (no rotation: cos_sin and pos are not read) or a multiple of 16
+ *         up to D.  The pairs are (i, i + rot/2), or (2i, 2i+1) with
+ *         FP8SM_ROPE_INTERLEAVED.
+ *   y     device [T][ld_y]; y == x with ld_y == ld_x works in place, other
+ *         overlaps are not allowed.
+ * ld_x, ld_y >= (Hq + Hk) * D and multiples of 8; x, y, the weights and
+ * cos_sin 16-byte aligned.  Hq, Hk >= 0, not both 0.
+ */
+#define FP8SM_ROPE_INTERLEAVED 0x1u
+fp8sm_status fp8sm_qk_norm_rope(const void* x, fp8sm_dtype in, int64_t T, int32_t Hq, int32_t Hk,
+                                int32_t D, int64_t ld_x, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos_sin,
+                                int64_t max_pos, const int32_t* pos, int32_t rot, uint32_t flags,
+                                void* y, int64_t ld_y, hipStream_t stream);
+
+/*
+ * Quantise new keys and values into the cache.  For each touched block, head,
+ * and K or V, with a' = max(max|x|, 1e-10) over the block's new values:
+ *   e = ceil(log2(RN32(a' / 448))), code = E4M3(clamp(x 2^-e, +-448)),
+ * the group rule of fp8sm_quant_group's UE8M0 scales.  A block that already
+ * holds tokens keeps its exponent if that is larger; if it is smaller, it is
+ * raised to e and the held codes are rounded again, code' = E4M3(code
+ * 2^(old - e)).  Infinities and NaN do not take part in a': an infinity becomes
+ * +-448, a NaN the NaN code.  What a block holds behind the sequence's end is
+ * left as it was and never read.
+ *   k, v  device bf16/fp16 [T][ld]: Hkv heads of D values (e.g. columns of the
+ *         QKV product's rows); 16-byte aligned, ld_k, ld_v multiples of 8.
+ * A block written by two sequences of one call is not defined.
+ */
+fp8sm_status fp8sm_kv_cache_write(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                  fp8sm_dtype in, int64_t T, int64_t nseq, const int32_t* cu,
+                                  const int32_t* lens, const int32_t* table, int64_t ld_table,
+                                  int64_t max_blocks, int64_t num_blocks, int32_t Hkv, int32_t D,
+                                  int32_t block, uint8_t* k_codes, uint8_t* v_codes,
+                                  uint8_t* k_exp, uint8_t* v_exp, hipStream_t stream);
+
+/*
+ * Read cached tokens back: row cu[b] + i of k and v becomes the token at
+ * position lens[b] - n_b + i, each value code * 2^(byte - 127) rounded once to
+ * `out` (exact in bf16 within its normal range).  With the arguments of a
+ * write it returns what that write stored; with n_b = lens[b] all of it.
+ *   k, v  device bf16/fp16 [T][ld], 16-byte aligned, ld multiples of 8; either
+ *         may be NULL (not wanted).
+ */
+fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
+                                 const uint8_t* k_exp, const uint8_t* v_exp, int64_t num_blocks,
+                                 int32_t Hkv, int32_t D, int32_t block, int64_t T, int64_t nseq,
+                                 const int32_t* cu, const int32_t* lens, const int32_t* table,
+                                 int64_t ld_table, int64_t max_blocks, fp8sm_dtype out, void* k,
+                                 int64_t ld_k, void* v, int64_t ld_v, hipStream_t stream);
+
+/*
+ * Attention of the batch's queries over the cache:
+ *   o[row, h] = sum_t softmax_t(scale q[row, h] . K[t]) V[t]
+ * with the keys and values of head h / (Hq / Hkv), over the sequence's cached
+ * tokens t < lens[b]; with FP8SM_ATTN_CAUSAL only t <= the row's position;
+ * with window > 0 (causal only) only the `window` last of those.  A row that
+ * sees nothing gets zeros and lse -inf.  Statistics and sums are fp32; the
+ * probabilities are rounded for the product with V, by at most half a step of
+ * bf16 (2^-8 of each) in bf16 calls and of fp16 (2^-11) in fp16 calls.
+ *   q, o  device bf16/fp16 [T][ld]: Hq heads of D values, 16-byte aligned, ld
+ *         multiples of 8.  Hq a multiple of Hkv.
+ *   lse   device fp32 [T][Hq] or NULL: ln of the sum of exp(scores).
+ *   max_q, max_kv  host's knowledge of max n_b (>= 1) and max lens[b] (>= 0),
+ *         for speed only: they choose kernels and splits, any values give a
+ *         correct result.
+ *   workspace  device, 16-byte aligned, fp8sm_attention_cache_workspace bytes
+ *         of the same sizes (may be 0: NULL).  Not kept between calls; calls
+ *         that may run at the same time need one each.
+ * Further errors: workspace_bytes too small -> ERR_SHAPE; window without
+ * causal, unknown flags -> ERR_UNSUPPORTED; window < 0, Hq % Hkv -> ERR_SHAPE;
+ * T * Hq > 2^30 -> ERR_RANGE.
+ */
+#define FP8SM_ATTN_CAUSAL 0x1u
+fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, int64_t T,
+                                   int64_t nseq, int32_t Hq, const int32_t* cu,
+                                   const int32_t* lens, const int32_t* table, int64_t ld_table,
+                                   int64_t max_blocks, const uint8_t* k_codes,
+                                   const uint8_t* v_codes, const uint8_t* k_exp,
+                                   const uint8_t* v_exp, int64_t num_blocks, int32_t Hkv,
+                                   int32_t D, int32_t block, int64_t max_q, int64_t max_kv,
+                                   float scale, uint32_t flags, int32_t window, void* o,
+                                   int64_t ld_o, float* lse, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace for an fp8sm_attention_cache call of these sizes (0 on
+ * invalid input: the call itself reports it). */
+size_t fp8sm_attention_cache_workspace(int64_t T, int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                                       int64_t max_q, int64_t max_kv);
+
 /* Bytes needed for the scales of fp8sm_quant_group (0 on invalid input). */
 size_t fp8sm_scale_bytes(fp8sm_scale_fmt fmt, fp8sm_scale_layout lay, int64_t M, int64_t K_out,
                          int32_t group);
