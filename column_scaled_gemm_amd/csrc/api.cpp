@@ -4,9 +4,12 @@
 // load-time / run-time gate mismatch described in the prhub digest of sglang
 // PR #33148, implementation section, is the failure this avoids).
 #include <hip/hip_runtime_api.h>
+#include <float.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <initializer_list>
 #include <mutex>
 
@@ -621,7 +624,8 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   fp8sm_status st = kv_args(T, nseq, cu, lens, table, ld_table, max_blocks, k_codes, v_codes,
                             k_exp, v_exp, num_blocks, Hkv, D, block, &a.kb, &a.c);
   if (st != FP8SM_OK) return st;
-  if (Hq < 1 || Hq % Hkv || window < 0 || max_q < 1 || max_kv < 0) return FP8SM_ERR_SHAPE;
+  if (Hq < 1 || Hq % Hkv || window < 0 || max_q < 1 || max_kv < 0 || !std::isfinite(scale))
+    return FP8SM_ERR_SHAPE;
   if (window > 0 && !(flags & FP8SM_ATTN_CAUSAL)) return FP8SM_ERR_UNSUPPORTED;
   if (Hq > kMaxHeads || T * Hq > kMaxDim) return FP8SM_ERR_RANGE;
   if (ld_q < (int64_t)Hq * D || ld_o < (int64_t)Hq * D) return FP8SM_ERR_SHAPE;
@@ -643,7 +647,9 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   a.lse = lse;
   a.Hq = Hq;
   a.G = Hq / Hkv;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  // 0 becomes the smallest normal factor, so that a masked -inf stays -inf
+  a.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+  a.negate = scale < 0.f;
   a.causal = (flags & FP8SM_ATTN_CAUSAL) != 0;
   a.window = window;
   a.nsplit = p.nsplit;

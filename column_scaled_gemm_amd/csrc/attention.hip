@@ -79,6 +79,16 @@ __device__ __forceinline__ Span row_span(const AttnArgs& a, const Seq& s, int r0
   return p;
 }
 
+// max of a value over the two half-wavefronts, and over the four quarters
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float quarter_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+
 // ---------------------------------------------------------------------------
 // Few rows: 16 QT rows of one sequence and key head per workgroup, the cached
 // tokens split over the grid and over the four wavefronts, 64 tokens a step.
@@ -111,6 +121,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   const int t_end = min(sp.hi, t_begin + sp.chunk);  // ns == 0: no step
 
   // rows of this lane: the query values, what they see, their running state
+  const uint32_t flip = a.negate ? 0x80008000u : 0u;
   op8 qf[QT][2 * NI];
   int see_lo[QT], see_hi[QT];
 #pragma unroll
@@ -125,6 +136,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     for (int k = 0; k < 2 * NI; ++k) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (ok) v = *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
+      v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
       qf[i][k] = __builtin_bit_cast(op8, v);
     }
   }
@@ -149,32 +161,50 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 
   const int32_t* table = a.kb.table + (int64_t)b * a.kb.ld_table;
   const int in_mask = (1 << (bs - 4)) - 1;
-  struct Step {
-    uint4 k[4][NI], v[DT];
-    float ks, vs;  // the lane's key rows' and value tokens' scales
-    bool bad;      // the lane's value tokens have no block
-  };
+  // Keys of step i + 1 are loaded when those of step i are used up, its values
+  // likewise, so one of them is always on its way; the block numbers are read a
+  // step earlier still.
   const int last_run = max((t_end - 1) >> 4, 0);
-  auto fetch = [&](Step& st, int t0) {
-    const int kr = min((t0 >> 4) + (x >> 2), last_run), vr = min((t0 >> 4) + g, last_run);
-    int kp = table[kr >> (bs - 4)], vp = table[vr >> (bs - 4)];
-    st.bad = vp < 0 || vp >= a.c.num_blocks;
+  const int mb = bs - 4;
+  uint4 kc[4][NI], vc[DT];
+  float ks = 1.f, vs = 1.f;  // the lane's key rows' and value tokens' scales
+  int kp = 0, vp = 0;        // blocks of the coming step; vp < 0: none
+  auto fetch_pages = [&](int t0) {
+    kp = table[min((t0 >> 4) + (x >> 2), last_run) >> mb];
+    vp = table[min((t0 >> 4) + g, last_run) >> mb];
     if (kp < 0 || kp >= a.c.num_blocks) kp = 0;
-    if (st.bad) vp = 0;
-    const int64_t kh = (int64_t)kp * a.c.heads + hk, vh = (int64_t)vp * a.c.heads + hk;
+    if (vp < 0 || vp >= a.c.num_blocks) vp = -1;
+  };
+  auto fetch_k = [&](int t0) {
+    const int kr = min((t0 >> 4) + (x >> 2), last_run);
+    const int64_t kh = (int64_t)kp * a.c.heads + hk;
     const uint8_t* kb = a.c.k + ((kh << bs) + ((kr & in_mask) << 4) + (x & 3)) * D + 16 * g;
-    const uint8_t* vb = a.c.v + ((vh << bs) + ((vr & in_mask) << 4)) * D + 16 * x;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) st.k[t][i] = load_stream16(kb + 4 * t * D + 64 * i);
-#pragma unroll
-    for (int d = 0; d < DT; ++d) st.v[d] = load_stream16(vb + 256 * d);
-    st.ks = exp_byte_value(a.c.ke[F16 ? vh : kh]);
-    st.vs = exp_byte_value(a.c.ve[vh]);
+      for (int i = 0; i < NI; ++i) kc[t][i] = load_stream16(kb + 4 * t * D + 64 * i);
+    ks = exp_byte_value(a.c.ke[F16 ? (int64_t)max(vp, 0) * a.c.heads + hk : kh]);
   };
-  auto compute = [&](Step& st, int t0) {
-    const bool partial = t0 + 64 > min(all_hi, t_end) || t0 < all_lo || __ballot(st.bad) != 0;
+  auto fetch_v = [&](int t0) {
+    const int vr = min((t0 >> 4) + g, last_run);
+    const int64_t vh = (int64_t)max(vp, 0) * a.c.heads + hk;
+    const uint8_t* vb = a.c.v + ((vh << bs) + ((vr & in_mask) << 4)) * D + 16 * x;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) vc[d] = load_stream16(vb + 256 * d);
+    vs = exp_byte_value(a.c.ve[vh]);
+  };
+  int t0 = t_begin + 64 * w;
+  if (t0 < t_end) {
+    fetch_pages(t0);
+    fetch_k(t0);
+    fetch_v(t0);
+  }
+  while (t0 < t_end) {
+    const int next = t0 + 256;
+    const bool more = next < t_end;
+    const bool bad = vp < 0;  // the lane's value tokens have no block
+    const bool partial = t0 + 64 > min(all_hi, t_end) || t0 < all_lo || __ballot(bad) != 0;
+    const float c = F16 ? a.scale_log2 * ks : a.scale_log2;
     f32x4 sc[QT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -182,22 +212,25 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       for (int i = 0; i < QT; ++i) sc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 2 * NI; ++k) {
-        const uint4 c = st.k[t][k >> 1];
-        const uint32_t c0 = (k & 1) ? c.z : c.x, c1 = (k & 1) ? c.w : c.y;
+        const uint4 q = kc[t][k >> 1];
+        const uint32_t c0 = (k & 1) ? q.z : q.x, c1 = (k & 1) ? q.w : q.y;
         if constexpr (F16) {
           const f16x8 kf = widen_f16(c0, c1, 1.0f);
 #pragma unroll
           for (int i = 0; i < QT; ++i)
             sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[i][k], sc[i][t], 0, 0, 0);
         } else {
-          const bf16x8 kf = widen_bf16(c0, c1, st.ks);
+          const bf16x8 kf = widen_bf16(c0, c1, ks);
 #pragma unroll
           for (int i = 0; i < QT; ++i)
             sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[i][k], sc[i][t], 0, 0, 0);
         }
       }
     }
-    const float c = F16 ? a.scale_log2 * st.ks : a.scale_log2;
+    if (more) {
+      fetch_pages(next);
+      fetch_k(next);
+    }
     bf16x8 ph[QT][2], pl[QT][2];
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
@@ -209,13 +242,12 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
           float v = sc[i][t][k] * c;
           if (partial) {
             const int tok = t0 + 16 * g + 4 * t + k;
-            if (tok < see_lo[i] || tok >= min(see_hi[i], t_end) || st.bad) v = -INFINITY;
+            if (tok < see_lo[i] || tok >= min(see_hi[i], t_end) || bad) v = -INFINITY;
           }
           sc[i][t][k] = v;
           mx = fmaxf(mx, v);
         }
-      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      mx = quarter_max(mx);
       const float mn = fmaxf(m[i], mx);
       const float ms = mn == -INFINITY ? 0.f : mn;
       const float al = __builtin_amdgcn_exp2f(m[i] - ms);
@@ -238,24 +270,24 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
         for (int k = 0; k < 4; ++k) o[i][d][k] *= al;
     }
     if (partial) {  // what no row sees may hold anything, NaN codes too
-      const int t = t0 + 16 * g, lo = st.bad ? 0x7FFFFFFF : sp.lo;
+      const int t = t0 + 16 * g, lo = bad ? 0x7FFFFFFF : sp.lo;
       uint32_t keep[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) keep[k] = token_bytes(t + 4 * k, lo, t_end);
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        st.v[d].x &= keep[0];
-        st.v[d].y &= keep[1];
-        st.v[d].z &= keep[2];
-        st.v[d].w &= keep[3];
+        vc[d].x &= keep[0];
+        vc[d].y &= keep[1];
+        vc[d].z &= keep[2];
+        vc[d].w &= keep[3];
       }
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t c0 = h ? st.v[d].z : st.v[d].x, c1 = h ? st.v[d].w : st.v[d].y;
-        const bf16x8 vf = widen_bf16(c0, c1, st.vs);
+        const uint32_t c0 = h ? vc[d].z : vc[d].x, c1 = h ? vc[d].w : vc[d].y;
+        const bf16x8 vf = widen_bf16(c0, c1, vs);
 #pragma unroll
         for (int i = 0; i < QT; ++i) {
           o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph[i][h], o[i][d], 0, 0, 0);
@@ -263,13 +295,8 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
             o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl[i][h], o[i][d], 0, 0, 0);
         }
       }
-  };
-  {
-    Step st;
-    for (int t0 = t_begin + 64 * w; t0 < t_end; t0 += 256) {
-      fetch(st, t0);
-      compute(st, t0);
-    }
+    if (more) fetch_v(next);
+    t0 = next;
   }
 
   // join the four wavefronts
@@ -326,31 +353,59 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 // Many rows: 128 rows of one sequence and key head per workgroup, 32 a
-// wavefront, 64 tokens a step.  Codes are staged in LDS, two steps deep, and
-// widened by the wavefronts that multiply them.  Bound by the matrix
-// instructions and the softmax's vector arithmetic.
+// wavefront, 64 tokens a step.  Wavefront w copies the step's run w of 16
+// tokens (keys and values, 2 KB each at D = 128) straight into an LDS ring of
+// three steps; a run lies in one block, so its address is wavefront-uniform.
+// Block numbers and scales are gathered 256 runs at a time into LDS.
 //
 // v_mfma_f32_32x32x16: lane l = 32 h + x holds row / column x and eight k
 // values of half h of both operands; of the result column x and rows
 // 8 v + 4 h + i in register 4 v + i.  Of 32 tokens, row m of the key tile is
 // token 16 ((m >> 2) & 1) + 4 (m >> 3) + m % 4, so lane half h has the scores
 // of the consecutive tokens 16 h .. 16 h + 15 in its registers 0 .. 15.
-// P is rounded to fp16 (p <= 1: an error of 2^-12 of p, half a step) and V is
-// widened to fp16 relative to the largest value scale of the row tile's
-// blocks, so neither leaves fp16's range; the accumulator is fp32.
-constexpr int kPrefillRows = 128, kPrefillStep = 64;
+//
+// P is rounded to fp16 (half a step: 2^-11 of p) and V is widened to fp16
+// relative to the largest value scale within reach of the row tile: exact
+// while the scales lie within 2^15 of each other (the smallest code's last
+// bit, 2^-9, still is a fp16 value).  Wider ranges take V in bf16 and P as the
+// sum of two bf16 values (WIDE).  Sums are fp32.
+//
+// The running maximum is moved only when a row's scores exceed it by more than
+// 2^kSlack (p <= 2^kSlack then: no precision is lost, fp16 reaches 2^15), so
+// most steps do not rescale the accumulator.
+constexpr int kPrefillRows = 128, kPrefillStep = 64, kPrefillSlots = 3;
+constexpr int kMetaSteps = 64;  // steps whose runs' blocks and scales one gather brings
+constexpr float kSlack = 8.0f;
+
+// 16-byte global -> LDS copy: reads base + off, lane i writes lds + 16 i.
+// Inline asm, so that the compiler does not wait for it before each LDS read;
+// wait_copies waits for what is needed.  m0 is used for nothing else here.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int OFF>
+__device__ __forceinline__ void copy16(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
+               :
+               : "s"(lds), "v"(off), "s"(base), "n"(OFF)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 template <bool F16, int D>
 __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
-  constexpr int DT = D / 32, NP = D / 32;      // channel tiles; 16-byte pieces of a lane's key row
-  constexpr int TILE = kPrefillStep * D;       // bytes of a step's keys or values
-  constexpr int CPT = TILE / 16 / 256;         // 16-byte pieces a thread stages of each
-  constexpr int CPR = D / 16;                  // pieces of a key row
+  constexpr int DT = D / 32, NP = D / 32;  // channel tiles; 16-byte pieces of a lane's key row
+  constexpr int RUN = 16 * D;              // bytes of a run's keys or values
+  constexpr int TILE = 4 * RUN;
+  constexpr int CPW = 2 * RUN / 1024;      // copies of a wavefront a step
   using op8 = std::conditional_t<F16, f16x8, bf16x8>;
-  __shared__ __attribute__((aligned(16))) uint8_t lk[2][TILE], lv[2][TILE];
-  __shared__ float sks[2][4], svs[2][4];       // scales of a step's four runs of 16 tokens
-  __shared__ int sbad[2];
-  __shared__ int sref[4];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kPrefillSlots][2][TILE];
+  __shared__ __attribute__((aligned(16))) int mpage[2][4 * kMetaSteps];  // block, -1: none
+  __shared__ float mks[2][4 * kMetaSteps], mvs[2][4 * kMetaSteps];
+  __shared__ int sref[8];
   const int tid = threadIdx.x, lane = tid & 63, x = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bs = a.c.block_shift;
@@ -368,34 +423,69 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   const int t_end = min(sp.hi, t_begin + sp.chunk);
   const int32_t* table = a.kb.table + (int64_t)b * a.kb.ld_table;
   const int in_mask = (1 << (bs - 4)) - 1;
+  const int steps = t_end > t_begin ? (t_end - t_begin + kPrefillStep - 1) / kPrefillStep : 0;
 
-  // the largest value exponent of the blocks in reach
-  int eref = 0;
-  if (t_begin < t_end) {
+  // the largest and smallest value exponents of the blocks in reach
+  int eref = 0, emin = 255;
+  if (steps > 0) {
     for (int p = (t_begin >> bs) + tid; p <= (t_end - 1) >> bs; p += 256) {
       const int page = table[p];
-      if (page >= 0 && page < a.c.num_blocks) eref = max(eref, (int)a.c.ve[(int64_t)page * a.c.heads + hk]);
+      if (page >= 0 && page < a.c.num_blocks) {
+        const int e = a.c.ve[(int64_t)page * a.c.heads + hk];
+        eref = max(eref, e);
+        emin = min(emin, e);
+      }
     }
 #pragma unroll
-    for (int k = 1; k < 64; k <<= 1) eref = max(eref, __shfl_xor(eref, k, 64));
-    if (lane == 0) sref[w] = eref;
+    for (int k = 1; k < 64; k <<= 1) {
+      eref = max(eref, __shfl_xor(eref, k, 64));
+      emin = min(emin, __shfl_xor(emin, k, 64));
+    }
+    if (lane == 0) sref[w] = eref, sref[4 + w] = emin;
     __syncthreads();
     eref = max(max(sref[0], sref[1]), max(sref[2], sref[3]));
+    emin = min(min(sref[4], sref[5]), min(sref[6], sref[7]));
+    eref = __builtin_amdgcn_readfirstlane(eref);
+    emin = __builtin_amdgcn_readfirstlane(emin);
   }
+  const bool wide = eref - emin > 15;
+
+  // gathers the blocks and scales of steps [kMetaSteps k, kMetaSteps (k + 1))
+  const int first_run = t_begin >> 4, last_run = max((t_end - 1) >> 4, 0);
+  auto gather = [&](int k) {
+    const int run = first_run + 4 * kMetaSteps * k + tid;
+    int page = -1;
+    float ks = 1.f, vs = 1.f;
+    if (run <= last_run) {
+      page = table[run >> (bs - 4)];
+      if (page < 0 || page >= a.c.num_blocks) page = -1;
+      if (page >= 0) {
+        const int64_t ph = (int64_t)page * a.c.heads + hk;
+        ks = exp_byte_value(a.c.ke[ph]);
+        const int ve = a.c.ve[ph];
+        vs = wide ? exp_byte_value(ve) : pow2f(ve - eref);
+      }
+    }
+    mpage[k & 1][tid] = page;
+    mks[k & 1][tid] = ks;
+    mvs[k & 1][tid] = vs;
+  };
 
   const int r = r0 + 32 * w + x;
   const bool ok = r < rows;
   const int tok = ok ? r / a.G : 0, head = hk * a.G + (ok ? r - tok * a.G : 0);
   const int pos = s.len - s.n + tok;
-  const int see_hi = ok ? (a.causal ? min(pos + 1, s.len) : s.len) : 0;
+  const int see_hi = min(ok ? (a.causal ? min(pos + 1, s.len) : s.len) : 0, t_end);
   const int see_lo = ok && a.window ? max(pos - a.window + 1, 0) : 0;
   op8 qf[2 * NP];
   {
     const uint16_t* q = a.q + (int64_t)(s.c0 + tok) * a.ld_q + (int64_t)head * D;
+    const uint32_t flip = a.negate ? 0x80008000u : 0u;
 #pragma unroll
     for (int k = 0; k < 2 * NP; ++k) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (ok) v = *reinterpret_cast<const uint4*>(q + 32 * (k >> 1) + 16 * h + 8 * (k & 1));
+      v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
       qf[k] = __builtin_bit_cast(op8, v);
     }
   }
@@ -407,7 +497,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
     if (a0 < a1) {
       const int first = s.len - s.n + a0 / a.G, last = s.len - s.n + (a1 - 1) / a.G;
       w_hi = a.causal ? max(min(s.len, last + 1), 0) : s.len;
-      all_hi = a.causal ? min(s.len, first + 1) : s.len;
+      all_hi = min(a.causal ? min(s.len, first + 1) : s.len, t_end);
       w_lo = a.window ? max(first - a.window + 1, 0) : 0;
       all_lo = a.window ? last - a.window + 1 : 0;
     }
@@ -418,86 +508,53 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[d][k] = 0.f;
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f;  // m: in units of log2 after the scale
 
-  // staging: thread t copies pieces t + 256 j
-  uint4 rk[CPT], rv[CPT];
-  float rks = 0.f, rvs = 0.f;
-  int rbad = 0;
-  const int last_run = max((t_end - 1) >> 4, 0);
-  auto load = [&](int t0) {
-#pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      const int c = tid + 256 * j;
-      {
-        const int row = c / CPR, cc = c % CPR;
-        const int key = D == 128 ? ((row & 3) | ((row >> 4) & 1) << 2) : (((row >> 1) & 1) | ((row >> 4) & 1) << 1);
-        const int run = min((t0 + row) >> 4, last_run);
-        int page = table[run >> (bs - 4)];
-        if (page < 0 || page >= a.c.num_blocks) page = 0;
-        const int64_t ph = (int64_t)page * a.c.heads + hk;
-        rk[j] = *reinterpret_cast<const uint4*>(
-            a.c.k + ((ph << bs) + ((run & in_mask) << 4) + (row & 15)) * D + 16 * (cc ^ key));
-      }
-      {
-        const int sub = c / D, d = c % D;
-        const int run = min((t0 >> 4) + sub, last_run);
-        int page = table[run >> (bs - 4)];
-        const bool bad = page < 0 || page >= a.c.num_blocks;
-        if (bad) page = 0;
-        const int64_t ph = (int64_t)page * a.c.heads + hk;
-        uint4 v = *reinterpret_cast<const uint4*>(a.c.v + ((ph << bs) + ((run & in_mask) << 4)) * D + 16 * d);
-        const int t = t0 + 16 * sub;
-        if (bad || t < sp.lo || t + 16 > t_end) {  // what no row sees may hold anything
-          const int lo = bad ? 0x7FFFFFFF : sp.lo;
-          v.x &= token_bytes(t, lo, t_end);
-          v.y &= token_bytes(t + 4, lo, t_end);
-          v.z &= token_bytes(t + 8, lo, t_end);
-          v.w &= token_bytes(t + 12, lo, t_end);
-        }
-        rv[j] = v;
-      }
-    }
-    if (tid < 64) {
-      const int run = min((t0 >> 4) + (tid & 3), last_run);
-      int page = table[run >> (bs - 4)];
-      const bool bad = page < 0 || page >= a.c.num_blocks;
-      if (bad) page = 0;
-      const int64_t ph = (int64_t)page * a.c.heads + hk;
-      rks = exp_byte_value(a.c.ke[ph]);
-      rvs = bad ? 1.f : pow2f(max((int)a.c.ve[ph] - eref, -126));
-      rbad = (int)(__ballot(bad) & 15);
-    }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)&ring[0][0][0]);
+  // a lane's place in a copy of key rows: LDS takes them in lane order, and 16-byte
+  // piece c of row r belongs at c ^ key(r), so that the eight rows that eight
+  // consecutive lanes read later lie in different banks
+  uint32_t koff;
+  if constexpr (D == 128) {
+    const int row = lane >> 3, key = (row & 3) | (w & 1) << 2;
+    koff = row * 128 + 16 * ((lane & 7) ^ key);
+  } else {
+    const int row = lane >> 2, key = ((row >> 1) & 1) | (w & 1) << 1;
+    koff = row * 64 + 16 * ((lane & 3) ^ key);
+  }
+  auto issue = [&](int i) {
+    const int run = __builtin_amdgcn_readfirstlane(first_run + 4 * i + w);
+    const int page = max(__builtin_amdgcn_readfirstlane(mpage[(i / kMetaSteps) & 1][4 * (i % kMetaSteps) + w]), 0);
+    const int64_t at = ((((int64_t)page * a.c.heads + hk) << bs) + ((run & in_mask) << 4)) * D;
+    const uint32_t dst = lds0 + (uint32_t)(i % kPrefillSlots) * (2 * TILE) + w * RUN;
+    copy16<0>(a.c.k + at, koff, dst);
+    if constexpr (D == 128) copy16<0>(a.c.k + at + 1024, koff, dst + 1024);
+    copy16<0>(a.c.v + at, lane * 16, dst + TILE);
+    if constexpr (D == 128) copy16<0>(a.c.v + at + 1024, lane * 16, dst + TILE + 1024);
   };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      *reinterpret_cast<uint4*>(&lk[buf][(tid + 256 * j) * 16]) = rk[j];
-      *reinterpret_cast<uint4*>(&lv[buf][(tid + 256 * j) * 16]) = rv[j];
-    }
-    if (tid < 4) {
-      sks[buf][tid] = rks;
-      svs[buf][tid] = rvs;
-    }
-    if (tid == 0) sbad[buf] = rbad;
-  };
-  // the lane's key row of 32 tokens, and its pieces' swizzled places
+
+  // the lane's key row of 32 tokens, and its pieces' places
   const int krow = 16 * ((x >> 2) & 1) + 4 * (x >> 3) + (x & 3);
   const int kkey = D == 128 ? ((krow & 3) | ((krow >> 4) & 1) << 2) : (((krow >> 1) & 1) | ((krow >> 4) & 1) << 1);
 
-  auto compute = [&](int buf, int t0) {
-    const int bad = sbad[buf];
-    const bool partial = t0 + kPrefillStep > all_hi || t0 < all_lo || t0 + kPrefillStep > t_end || bad;
+  auto compute = [&](int i, auto wide_tag) {
+    constexpr bool WIDE = decltype(wide_tag)::value;
+    const int t0 = t_begin + i * kPrefillStep;
+    const uint8_t* lk = ring[i % kPrefillSlots][0];
+    const uint8_t* lv = ring[i % kPrefillSlots][1];
+    const int mb = (i / kMetaSteps) & 1, mi = 4 * (i % kMetaSteps);
+    const int4 pages = *reinterpret_cast<const int4*>(&mpage[mb][mi]);
+    const bool gone_any = __builtin_amdgcn_readfirstlane(min(min(pages.x, pages.y), min(pages.z, pages.w))) < 0;
+    const bool partial = t0 + kPrefillStep > all_hi || t0 < all_lo || gone_any;
     f32x16 sc[2];
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) sc[grp][k] = 0.f;
-      const float ks = F16 ? 1.0f : sks[buf][2 * grp + (krow >> 4)];
+      const float ks = F16 ? 1.0f : mks[mb][mi + 2 * grp + (krow >> 4)];
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        const uint4 c = *reinterpret_cast<const uint4*>(
-            &lk[buf][(32 * grp + krow) * D + 16 * ((2 * u + h) ^ kkey)]);
+        const uint4 c = *reinterpret_cast<const uint4*>(lk + (32 * grp + krow) * D + 16 * ((2 * u + h) ^ kkey));
         if constexpr (F16) {
           sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, ks), qf[2 * u], sc[grp], 0, 0, 0);
           sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, ks), qf[2 * u + 1], sc[grp], 0, 0, 0);
@@ -510,67 +567,116 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
     float mx = -INFINITY;
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
-      const float c = F16 ? a.scale_log2 * sks[buf][2 * grp + h] : a.scale_log2;
-      const bool gone = (bad >> (2 * grp + h)) & 1;
+      if constexpr (F16) {  // the key scale of the lane's run of 16 tokens
+        const float ks = mks[mb][mi + 2 * grp + h];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        float v = sc[grp][k] * c;
-        if (partial) {
-          const int t = t0 + 32 * grp + 16 * h + k;
-          if (t < see_lo || t >= min(see_hi, t_end) || gone) v = -INFINITY;
-        }
-        sc[grp][k] = v;
-        mx = fmaxf(mx, v);
+        for (int k = 0; k < 16; ++k) sc[grp][k] *= ks;
       }
+      if (partial) {
+        const int p = grp == 0 ? (h ? pages.y : pages.x) : (h ? pages.w : pages.z);
+        const int lo = p < 0 ? 0x7FFFFFFF : see_lo, t = t0 + 32 * grp + 16 * h;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (t + k < lo || t + k >= see_hi) sc[grp][k] = -INFINITY;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) mx = fmaxf(mx, sc[grp][k]);
     }
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-    const float mn = fmaxf(m, mx);
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    const float al = __builtin_amdgcn_exp2f(m - ms);
-    m = mn;
+    mx = half_max(mx) * a.scale_log2;
+    if (__any(mx > m + kSlack)) {  // (also the first finite score of a row: m = -inf)
+      const float mn = fmaxf(m, mx);
+      const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[d][k] *= al;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
-    f16x8 p[4];
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp)
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float e = __builtin_amdgcn_exp2f(sc[grp][k] - ms);
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[grp][k], a.scale_log2, -ms));
         sum += e;
-        p[2 * grp + (k >> 3)][k & 7] = (_Float16)e;
+        sc[grp][k] = e;
       }
-    l = __builtin_fmaf(l, al, sum);
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) o[d][k] *= al;
+    l += sum;
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
-      const float vs = svs[buf][2 * grp + h];
+      const float vs = mvs[mb][mi + 2 * grp + h];
+      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+      if (partial) {  // what no row sees may hold anything, NaN codes too
+        const int p = grp == 0 ? (h ? pages.y : pages.x) : (h ? pages.w : pages.z);
+        const int t = t0 + 32 * grp + 16 * h, lo = p < 0 ? 0x7FFFFFFF : sp.lo;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const uint4 c = *reinterpret_cast<const uint4*>(&lv[buf][((2 * grp + h) * D + 32 * d + x) * 16]);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, vs), p[2 * grp], o[d], 0, 0, 0);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, vs), p[2 * grp + 1], o[d], 0, 0, 0);
+        for (int k = 0; k < 4; ++k) keep[k] = token_bytes(t + 4 * k, lo, t_end);
+      }
+      if constexpr (WIDE) {
+        bf16x8 ph[2], pl[2];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const __bf16 hi = (__bf16)sc[grp][k];
+          ph[k >> 3][k & 7] = hi;
+          pl[k >> 3][k & 7] = (__bf16)(sc[grp][k] - (float)hi);
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          uint4 c = *reinterpret_cast<const uint4*>(lv + ((2 * grp + h) * D + 32 * d + x) * 16);
+          c.x &= keep[0], c.y &= keep[1], c.z &= keep[2], c.w &= keep[3];
+          const bf16x8 v0 = widen_bf16(c.x, c.y, vs), v1 = widen_bf16(c.z, c.w, vs);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, ph[0], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, pl[0], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, ph[1], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, pl[1], o[d], 0, 0, 0);
+        }
+      } else {
+        f16x8 p[2];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[k >> 3][k & 7] = (_Float16)sc[grp][k];
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          uint4 c = *reinterpret_cast<const uint4*>(lv + ((2 * grp + h) * D + 32 * d + x) * 16);
+          if (partial) c.x &= keep[0], c.y &= keep[1], c.z &= keep[2], c.w &= keep[3];
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, vs), p[0], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, vs), p[1], o[d], 0, 0, 0);
+        }
       }
     }
   };
 
-  if (t_begin < t_end) {
-    load(t_begin);
-    store(0);
-    int buf = 0;
-    for (int t0 = t_begin; t0 < t_end; t0 += kPrefillStep, buf ^= 1) {
-      __syncthreads();  // the step's pieces are there; the other buffer is read no more
-      const bool more = t0 + kPrefillStep < t_end;
-      if (more) load(t0 + kPrefillStep);
-      if (t0 < w_hi && t0 + kPrefillStep > w_lo) compute(buf, t0);
-      if (more) store(buf ^ 1);
+  auto walk = [&](auto wide_tag) {
+    gather(0);
+    __syncthreads();
+    issue(0);
+    if (steps > 1) issue(1);
+    for (int i = 0; i < steps; ++i) {
+      if (i + 1 < steps)
+        wait_copies<CPW>();
+      else
+        wait_copies<0>();
+      __syncthreads();  // step i is in LDS, and nobody reads step i - 1 any more
+      if (i % kMetaSteps == kMetaSteps / 2 && i + kMetaSteps / 2 < steps) gather(i / kMetaSteps + 1);
+      if (i + 2 < steps) issue(i + 2);
+      const int t0 = t_begin + i * kPrefillStep;
+      if (t0 < w_hi && t0 + kPrefillStep > w_lo) compute(i, wide_tag);
     }
+  };
+  if (steps > 0) {
+    if (wide)
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
   }
-  l += __shfl_xor(l, 32, 64);
+  {
+    const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
+  }
   if (!ok) return;
   const int64_t t = s.c0 + tok;
-  const float vref = exp_byte_value(eref);
+  const float vref = wide ? 1.f : exp_byte_value(eref);
   if (ns <= 1) {
     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
     uint16_t* dst = a.out + t * a.ld_o + head * D;

@@ -174,7 +174,8 @@ struct AttnArgs {
   KvBatch kb;
   KvCache c;
   int Hq, G;
-  float scale_log2;  // softmax scale * log2(e)
+  float scale_log2;  // |softmax scale| * log2(e), above 0
+  int negate;        // the scale is negative: the queries are negated instead
   int causal, window;
   // split over the cached tokens: a row tile's split s covers `chunk` tokens;
   // part_o [split][T][Hq][D], part_ml [split][T][Hq] hold unjoined results

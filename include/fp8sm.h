@@ -423,7 +423,8 @@ fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
  *         of the same sizes (may be 0: NULL).  Not kept between calls; calls
  *         that may run at the same time need one each.
  * Further errors: workspace_bytes too small -> ERR_SHAPE; window without
- * causal, unknown flags -> ERR_UNSUPPORTED; window < 0, Hq % Hkv -> ERR_SHAPE;
+ * causal, unknown flags -> ERR_UNSUPPORTED; window < 0, Hq % Hkv, a scale that is
+ * not finite -> ERR_SHAPE;
  * T * Hq > 2^30 -> ERR_RANGE.
  */
 #define FP8SM_ATTN_CAUSAL 0x1u
