@@ -53,7 +53,7 @@ constexpr int64_t kMaxK = 65536;
 // GEMM operand row strides (bytes): the kernels address up to 64 rows of A or
 // B with 32-bit offsets from one base, so 64 * stride + K must stay below 2^31.
 constexpr int64_t kMaxGemmLd = (int64_t)1 << 24;
-constexpr int64_t kMaxTokens = (int64_t)1 << 24;
+constexpr int64_t kMaxTokens = (int64_t)1 << 23;
 constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
 constexpr int32_t kMaxHeads = 1024;
 constexpr int64_t kMaxBatch = 65535;  // one grid row (blockIdx.y) per batch

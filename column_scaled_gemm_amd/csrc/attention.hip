@@ -25,6 +25,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// The running maximum is moved only when a row's scores exceed it by more than
+// 2^kSlack (p <= 2^kSlack then: no precision is lost, fp16 reaches 2^15), so
+// most steps do not rescale the accumulator.
+constexpr float kSlack = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Eight codes widened times a power of two, exactly unless the result leaves
@@ -79,6 +83,14 @@ __device__ __forceinline__ Span row_span(const AttnArgs& a, const Seq& s, int r0
   return p;
 }
 
+// Grids are one list of workgroups; more than a grid's first dimension takes
+// go on in its second.
+constexpr uint32_t kGridX = 1 << 16;
+__device__ __forceinline__ int64_t workgroup_id() { return blockIdx.x + (int64_t)blockIdx.y * kGridX; }
+static dim3 grid_of(int64_t n) {
+  return n <= kGridX ? dim3((uint32_t)n) : dim3(kGridX, (uint32_t)((n + kGridX - 1) / kGridX));
+}
+
 // max of a value over the two half-wavefronts, and over the four quarters
 __device__ __forceinline__ float half_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -100,20 +112,34 @@ __device__ __forceinline__ float quarter_max(float v) {
 // 4 g .. 4 g + 3.  Of a step's 64 tokens, key tile t (0..3) takes as its row m
 // token 16 (m / 4) + 4 t + m % 4, so that lane quarter g ends up with the
 // scores of the consecutive tokens 16 g .. 16 g + 15.
+constexpr int kDecodeRuns = 256;  // runs of 16 tokens a gather brings
+
+__host__ __device__ __forceinline__ int decode_stride(const AttnArgs& a) { return a.c.heads * a.nsplit | 1; }
+
 template <bool F16, int D, int QT>
-__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
   constexpr int NI = D / 64, DT = D / 16;
+  __shared__ int64_t mat[kDecodeRuns];  // a run's place in both code arrays, -1: no block
+  __shared__ float mks[kDecodeRuns], mvs[kDecodeRuns];
   using op8 = std::conditional_t<F16, f16x8, bf16x8>;
   const int lane = threadIdx.x & 63, x = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int bs = a.c.block_shift;
+  // heads, then splits, then row tiles: consecutive workgroups go to the eight
+  // XCDs in turn.  An odd number of them a row tile (one idle) keeps any stride
+  // of idle tiles or of short sequences from falling on the same XCDs (with an
+  // even one, 154 us where 106 were due).
+  const int per = decode_stride(a), id = (int)(workgroup_id() % per);
+  const int64_t slot = workgroup_id() / per;
+  if (id >= a.c.heads * a.nsplit) return;
+  const int hk = id % a.c.heads, split = id / a.c.heads;
   int64_t f0;
-  const int b = find_seq(a.kb, blockIdx.x, a.G, QT == 2 ? 5 : 4, 1, &f0);
+  const int b = find_seq(a.kb, slot, a.G, QT == 2 ? 5 : 4, 1, &f0);
   const Seq s = load_seq(a.kb, b, bs);
   const int rows = s.n * a.G;
-  const int r0 = (int)(blockIdx.x - f0) * (16 * QT);
-  if (r0 >= rows || rows > a.row_limit) return;
-  const int hk = blockIdx.y, split = blockIdx.z;
+  const int64_t r64 = (slot - f0) * (16 * QT);
+  if (r64 >= rows || rows > a.row_limit) return;
+  const int r0 = (int)r64;
   const Span sp = row_span(a, s, r0, min(r0 + 16 * QT, rows));
   const int ns = sp.splits;
   if (split >= max(ns, 1)) return;
@@ -121,6 +147,10 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   const int t_end = min(sp.hi, t_begin + sp.chunk);  // ns == 0: no step
 
   // rows of this lane: the query values, what they see, their running state
+  // (32 rows' query values would not fit beside the rest, and reloading what
+  // was spilled to memory waits for every code on its way: they stay in LDS)
+  constexpr bool QLDS = QT == 2;
+  __shared__ uint4 sq[QLDS ? QT : 1][QLDS ? 2 * NI : 1][64];
   const uint32_t flip = a.negate ? 0x80008000u : 0u;
   op8 qf[QT][2 * NI];
   int see_lo[QT], see_hi[QT];
@@ -129,7 +159,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     const int r = r0 + 16 * i + x;
     const bool ok = r < rows;
     const int tok = ok ? r / a.G : 0, p = s.len - s.n + tok;
-    see_hi[i] = ok ? (a.causal ? min(p + 1, s.len) : s.len) : 0;
+    see_hi[i] = min(ok ? (a.causal ? min(p + 1, s.len) : s.len) : 0, t_end);
     see_lo[i] = ok && a.window ? max(p - a.window + 1, 0) : 0;
     const uint16_t* q = a.q + (int64_t)(s.c0 + tok) * a.ld_q + (int64_t)(hk * a.G + (ok ? r - tok * a.G : 0)) * D;
 #pragma unroll
@@ -137,7 +167,11 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (ok) v = *reinterpret_cast<const uint4*>(q + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
       v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-      qf[i][k] = __builtin_bit_cast(op8, v);
+      if constexpr (QLDS) {
+        if (w == 0) sq[i][k][lane] = v;
+      } else {
+        qf[i][k] = __builtin_bit_cast(op8, v);
+      }
     }
   }
   f32x4 o[QT][DT];
@@ -155,148 +189,178 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     const int first = s.len - s.n + r0 / a.G;
     const int last = s.len - s.n + (min(r0 + 16 * QT, rows) - 1) / a.G;
     if (a.causal) all_hi = first + 1;
-    all_hi = min(all_hi, s.len);
+    all_hi = min(min(all_hi, s.len), t_end);
     if (a.window) all_lo = last - a.window + 1;
   }
 
   const int32_t* table = a.kb.table + (int64_t)b * a.kb.ld_table;
   const int in_mask = (1 << (bs - 4)) - 1;
   // Keys of step i + 1 are loaded when those of step i are used up, its values
-  // likewise, so one of them is always on its way; the block numbers are read a
-  // step earlier still.
+  // likewise, so one of them is always on its way.  Places and scales of the
+  // runs of 16 tokens are gathered into LDS before (the plan's chunks need one
+  // gather): reading a block's number just before its codes made every step
+  // wait for two trips to memory (257 us instead of NEWLONG on 2 x 131072 tokens
+  // of 8 heads).
   const int last_run = max((t_end - 1) >> 4, 0);
-  const int mb = bs - 4;
   uint4 kc[4][NI], vc[DT];
-  float ks = 1.f, vs = 1.f;  // the lane's key rows' and value tokens' scales
-  int kp = 0, vp = 0;        // blocks of the coming step; vp < 0: none
-  auto fetch_pages = [&](int t0) {
-    kp = table[min((t0 >> 4) + (x >> 2), last_run) >> mb];
-    vp = table[min((t0 >> 4) + g, last_run) >> mb];
-    if (kp < 0 || kp >= a.c.num_blocks) kp = 0;
-    if (vp < 0 || vp >= a.c.num_blocks) vp = -1;
-  };
-  auto fetch_k = [&](int t0) {
-    const int kr = min((t0 >> 4) + (x >> 2), last_run);
-    const int64_t kh = (int64_t)kp * a.c.heads + hk;
-    const uint8_t* kb = a.c.k + ((kh << bs) + ((kr & in_mask) << 4) + (x & 3)) * D + 16 * g;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) kc[t][i] = load_stream16(kb + 4 * t * D + 64 * i);
-    ks = exp_byte_value(a.c.ke[F16 ? (int64_t)max(vp, 0) * a.c.heads + hk : kh]);
-  };
-  auto fetch_v = [&](int t0) {
-    const int vr = min((t0 >> 4) + g, last_run);
-    const int64_t vh = (int64_t)max(vp, 0) * a.c.heads + hk;
-    const uint8_t* vb = a.c.v + ((vh << bs) + ((vr & in_mask) << 4)) * D + 16 * x;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) vc[d] = load_stream16(vb + 256 * d);
-    vs = exp_byte_value(a.c.ve[vh]);
-  };
-  int t0 = t_begin + 64 * w;
-  if (t0 < t_end) {
-    fetch_pages(t0);
-    fetch_k(t0);
-    fetch_v(t0);
-  }
-  while (t0 < t_end) {
-    const int next = t0 + 256;
-    const bool more = next < t_end;
-    const bool bad = vp < 0;  // the lane's value tokens have no block
-    const bool partial = t0 + 64 > min(all_hi, t_end) || t0 < all_lo || __ballot(bad) != 0;
-    const float c = F16 ? a.scale_log2 * ks : a.scale_log2;
-    f32x4 sc[QT][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-      for (int i = 0; i < QT; ++i) sc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < 2 * NI; ++k) {
-        const uint4 q = kc[t][k >> 1];
-        const uint32_t c0 = (k & 1) ? q.z : q.x, c1 = (k & 1) ? q.w : q.y;
-        if constexpr (F16) {
-          const f16x8 kf = widen_f16(c0, c1, 1.0f);
-#pragma unroll
-          for (int i = 0; i < QT; ++i)
-            sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[i][k], sc[i][t], 0, 0, 0);
-        } else {
-          const bf16x8 kf = widen_bf16(c0, c1, ks);
-#pragma unroll
-          for (int i = 0; i < QT; ++i)
-            sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[i][k], sc[i][t], 0, 0, 0);
+  for (int seg = t_begin; seg < t_end; seg += 16 * kDecodeRuns) {
+    if (seg > t_begin) __syncthreads();  // nobody reads the last segment's any more
+    {
+      const int run = (seg >> 4) + threadIdx.x;
+      int64_t at = -1;
+      float ks = 1.f, vs = 1.f;
+      if (run <= last_run) {
+        const int page = table[run >> (bs - 4)];
+        if (page >= 0 && page < a.c.num_blocks) {
+          const int64_t ph = (int64_t)page * a.c.heads + hk;
+          at = ((ph << bs) + ((run & in_mask) << 4)) * D;
+          ks = exp_byte_value(a.c.ke[ph]);
+          vs = exp_byte_value(a.c.ve[ph]);
         }
       }
+      mat[threadIdx.x] = at;
+      mks[threadIdx.x] = ks;
+      mvs[threadIdx.x] = vs;
     }
-    if (more) {
-      fetch_pages(next);
-      fetch_k(next);
-    }
-    bf16x8 ph[QT][2], pl[QT][2];
-#pragma unroll
-    for (int i = 0; i < QT; ++i) {
-      float mx = -INFINITY;
+    __syncthreads();
+    const int seg_end = min(t_end, seg + 16 * kDecodeRuns);
+    auto fetch_k = [&](int t0) {
+      const int64_t at = max(mat[((t0 - seg) >> 4) + (x >> 2)], (int64_t)0);
+      const uint8_t* kb = a.c.k + at + (x & 3) * D + 16 * g;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float v = sc[i][t][k] * c;
-          if (partial) {
-            const int tok = t0 + 16 * g + 4 * t + k;
-            if (tok < see_lo[i] || tok >= min(see_hi[i], t_end) || bad) v = -INFINITY;
+        for (int i = 0; i < NI; ++i) kc[t][i] = load_stream16(kb + 4 * t * D + 64 * i);
+    };
+    auto fetch_v = [&](int t0) {
+      const int64_t at = max(mat[((t0 - seg) >> 4) + g], (int64_t)0);
+      const uint8_t* vb = a.c.v + at + 16 * x;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vc[d] = load_stream16(vb + 256 * d);
+    };
+    int t0 = seg + 64 * w;
+    if (t0 < seg_end) {
+      fetch_k(t0);
+      fetch_v(t0);
+    }
+    // (MORE at compile time: were the loads of the next step conditional, the
+    // compiler would have to wait as if they had not been issued)
+    auto step = [&](auto more) {
+      constexpr bool MORE = decltype(more)::value;
+      const int next = t0 + 256, mi = (t0 - seg) >> 4;
+      const bool bad = mat[mi + g] < 0;  // the lane's value tokens have no block
+      const float ks = mks[mi + (F16 ? g : x >> 2)], vs = mvs[mi + g];
+      const bool partial = t0 + 64 > all_hi || t0 < all_lo || __any(bad);
+      if constexpr (QLDS) {
+        asm volatile("" ::: "memory");  // every step reads them anew
+#pragma unroll
+        for (int i = 0; i < QT; ++i)
+#pragma unroll
+          for (int k = 0; k < 2 * NI; ++k) qf[i][k] = __builtin_bit_cast(op8, sq[i][k][lane]);
+      }
+      f32x4 sc[QT][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int i = 0; i < QT; ++i) sc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2 * NI; ++k) {
+          const uint4 q = kc[t][k >> 1];
+          const uint32_t c0 = (k & 1) ? q.z : q.x, c1 = (k & 1) ? q.w : q.y;
+          if constexpr (F16) {
+            const f16x8 kf = widen_f16(c0, c1, 1.0f);
+#pragma unroll
+            for (int i = 0; i < QT; ++i)
+              sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[i][k], sc[i][t], 0, 0, 0);
+          } else {
+            const bf16x8 kf = widen_bf16(c0, c1, ks);
+#pragma unroll
+            for (int i = 0; i < QT; ++i)
+              sc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[i][k], sc[i][t], 0, 0, 0);
           }
-          sc[i][t][k] = v;
-          mx = fmaxf(mx, v);
         }
-      mx = quarter_max(mx);
-      const float mn = fmaxf(m[i], mx);
-      const float ms = mn == -INFINITY ? 0.f : mn;
-      const float al = __builtin_amdgcn_exp2f(m[i] - ms);
-      m[i] = mn;
-      float sum = 0.f;
+      }
+      if constexpr (MORE) fetch_k(next);
+      bf16x8 ph[QT][2], pl[QT][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int i = 0; i < QT; ++i) {
+        if constexpr (F16) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float p = __builtin_amdgcn_exp2f(sc[i][t][k] - ms);
-          sum += p;
-          const __bf16 hi = (__bf16)p;
-          ph[i][t >> 1][4 * (t & 1) + k] = hi;
-          if constexpr (F16) pl[i][t >> 1][4 * (t & 1) + k] = (__bf16)(p - (float)hi);
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[i][t][k] *= ks;
         }
-      l[i] = __builtin_fmaf(l[i], al, sum);
+        if (partial) {
+          const int lo = bad ? 0x7FFFFFFF : see_lo[i], tok = t0 + 16 * g;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (tok + 4 * t + k < lo || tok + 4 * t + k >= see_hi[i]) sc[i][t][k] = -INFINITY;
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx = fmaxf(mx, sc[i][t][k]);
+        mx = quarter_max(mx) * a.scale_log2;
+        if (__any(mx > m[i] + kSlack)) {  // (also a row's first score: m = -inf)
+          const float mn = fmaxf(m[i], mx);
+          const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[i] - mn);
+          m[i] = mn;
+          l[i] *= al;
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][d][k] *= al;
+        }
+        const float ms = m[i] == -INFINITY ? 0.f : m[i];
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][t][k], a.scale_log2, -ms));
+            sum += p;
+            const __bf16 hi = (__bf16)p;
+            ph[i][t >> 1][4 * (t & 1) + k] = hi;
+            if constexpr (F16) pl[i][t >> 1][4 * (t & 1) + k] = (__bf16)(p - (float)hi);
+          }
+        l[i] += sum;
+      }
+      if (partial) {  // what no row sees may hold anything, NaN codes too
+        const int t = t0 + 16 * g, lo = bad ? 0x7FFFFFFF : sp.lo;
+        uint32_t keep[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) keep[k] = token_bytes(t + 4 * k, lo, t_end);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          vc[d].x &= keep[0];
+          vc[d].y &= keep[1];
+          vc[d].z &= keep[2];
+          vc[d].w &= keep[3];
+        }
+      }
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][d][k] *= al;
-    }
-    if (partial) {  // what no row sees may hold anything, NaN codes too
-      const int t = t0 + 16 * g, lo = bad ? 0x7FFFFFFF : sp.lo;
-      uint32_t keep[4];
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t c0 = h ? vc[d].z : vc[d].x, c1 = h ? vc[d].w : vc[d].y;
+          const bf16x8 vf = widen_bf16(c0, c1, vs);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) keep[k] = token_bytes(t + 4 * k, lo, t_end);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        vc[d].x &= keep[0];
-        vc[d].y &= keep[1];
-        vc[d].z &= keep[2];
-        vc[d].w &= keep[3];
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t c0 = h ? vc[d].z : vc[d].x, c1 = h ? vc[d].w : vc[d].y;
-        const bf16x8 vf = widen_bf16(c0, c1, vs);
-#pragma unroll
-        for (int i = 0; i < QT; ++i) {
-          o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph[i][h], o[i][d], 0, 0, 0);
-          if constexpr (F16)
-            o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl[i][h], o[i][d], 0, 0, 0);
+          for (int i = 0; i < QT; ++i) {
+            o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph[i][h], o[i][d], 0, 0, 0);
+            if constexpr (F16)
+              o[i][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl[i][h], o[i][d], 0, 0, 0);
+          }
         }
-      }
-    if (more) fetch_v(next);
-    t0 = next;
+      if constexpr (MORE) fetch_v(next);
+      t0 = next;
+    };
+    if (t0 < seg_end) {
+      while (t0 + 256 < seg_end) step(std::true_type{});
+      step(std::false_type{});
+    }
   }
 
   // join the four wavefronts
@@ -356,7 +420,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 // wavefront, 64 tokens a step.  Wavefront w copies the step's run w of 16
 // tokens (keys and values, 2 KB each at D = 128) straight into an LDS ring of
 // three steps; a run lies in one block, so its address is wavefront-uniform.
-// Block numbers and scales are gathered 256 runs at a time into LDS.
+// Block numbers and scales are gathered 128 runs at a time into LDS.
 //
 // v_mfma_f32_32x32x16: lane l = 32 h + x holds row / column x and eight k
 // values of half h of both operands; of the result column x and rows
@@ -370,12 +434,8 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 // bit, 2^-9, still is a fp16 value).  Wider ranges take V in bf16 and P as the
 // sum of two bf16 values (WIDE).  Sums are fp32.
 //
-// The running maximum is moved only when a row's scores exceed it by more than
-// 2^kSlack (p <= 2^kSlack then: no precision is lost, fp16 reaches 2^15), so
-// most steps do not rescale the accumulator.
 constexpr int kPrefillRows = 128, kPrefillStep = 64, kPrefillSlots = 3;
-constexpr int kMetaSteps = 64;  // steps whose runs' blocks and scales one gather brings
-constexpr float kSlack = 8.0f;
+constexpr int kMetaSteps = 32;  // steps whose runs' blocks and scales one gather brings
 
 // 16-byte global -> LDS copy: reads base + off, lane i writes lds + 16 i.
 // Inline asm, so that the compiler does not wait for it before each LDS read;
@@ -395,6 +455,10 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+__host__ __device__ __forceinline__ int64_t prefill_slots(const AttnArgs& a) {
+  return (int64_t)a.kb.T * a.G / kPrefillRows + a.kb.B;
+}
+
 template <bool F16, int D>
 __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   constexpr int DT = D / 32, NP = D / 32;  // channel tiles; 16-byte pieces of a lane's key row
@@ -405,17 +469,30 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[kPrefillSlots][2][TILE];
   __shared__ __attribute__((aligned(16))) int mpage[2][4 * kMetaSteps];  // block, -1: none
   __shared__ float mks[2][4 * kMetaSteps], mvs[2][4 * kMetaSteps];
-  __shared__ int sref[8];
+  __shared__ int sref[12];
   const int tid = threadIdx.x, lane = tid & 63, x = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bs = a.c.block_shift;
+  // The list is head, split, row tile with the last tile (most tokens to see)
+  // first.  Workgroups go to the eight XCDs in turn; where that leaves no XCD
+  // with more work, each takes a contiguous part of the list, so that the tiles
+  // that read the same keys share an L2 (8320 tokens, 56 heads: 1237 us in
+  // list order, 1147 so; tiles in ascending order 1197).
+  const int64_t slots = prefill_slots(a), n = slots * a.c.heads * a.nsplit, id = workgroup_id();
+  if (id >= n) return;
+  const int pairs = a.c.heads * a.nsplit;
+  const int64_t part = n >> 3, rest = n & 7;
+  const int64_t at = pairs % 8 == 0 || pairs >= 64 ? (id & 7) * part + min(id & 7, rest) + (id >> 3) : id;
+  const int64_t pair = at / slots, k = at - pair * slots;
+  const int64_t slot = slots - 1 - k;
+  const int hk = (int)(pair / a.nsplit), split = (int)(pair - (int64_t)hk * a.nsplit);
   int64_t f0;
-  const int b = find_seq(a.kb, blockIdx.x, a.G, 7, 1, &f0);
+  const int b = find_seq(a.kb, slot, a.G, 7, 1, &f0);
   const Seq s = load_seq(a.kb, b, bs);
   const int rows = s.n * a.G;
-  const int r0 = (int)(blockIdx.x - f0) * kPrefillRows;
-  if (r0 >= rows || rows <= a.row_limit) return;
-  const int hk = blockIdx.y, split = blockIdx.z;
+  const int64_t r64 = (slot - f0) * kPrefillRows;
+  if (r64 >= rows || rows <= a.row_limit) return;
+  const int r0 = (int)r64;
   const Span sp = row_span(a, s, r0, min(r0 + kPrefillRows, rows));
   const int ns = sp.splits;
   if (split >= max(ns, 1)) return;
@@ -425,8 +502,9 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   const int in_mask = (1 << (bs - 4)) - 1;
   const int steps = t_end > t_begin ? (t_end - t_begin + kPrefillStep - 1) / kPrefillStep : 0;
 
-  // the largest and smallest value exponents of the blocks in reach
-  int eref = 0, emin = 255;
+  // the largest and smallest value exponents of the blocks in reach, and
+  // whether one is missing
+  int eref = 0, emin = 255, missing = 0;
   if (steps > 0) {
     for (int p = (t_begin >> bs) + tid; p <= (t_end - 1) >> bs; p += 256) {
       const int page = table[p];
@@ -434,17 +512,21 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
         const int e = a.c.ve[(int64_t)page * a.c.heads + hk];
         eref = max(eref, e);
         emin = min(emin, e);
+      } else {
+        missing = 1;
       }
     }
+    missing = __any(missing);
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) {
       eref = max(eref, __shfl_xor(eref, k, 64));
       emin = min(emin, __shfl_xor(emin, k, 64));
     }
-    if (lane == 0) sref[w] = eref, sref[4 + w] = emin;
+    if (lane == 0) sref[w] = eref, sref[4 + w] = emin, sref[8 + w] = missing;
     __syncthreads();
     eref = max(max(sref[0], sref[1]), max(sref[2], sref[3]));
     emin = min(min(sref[4], sref[5]), min(sref[6], sref[7]));
+    missing = __builtin_amdgcn_readfirstlane(sref[8] | sref[9] | sref[10] | sref[11]);
     eref = __builtin_amdgcn_readfirstlane(eref);
     emin = __builtin_amdgcn_readfirstlane(emin);
   }
@@ -453,6 +535,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   // gathers the blocks and scales of steps [kMetaSteps k, kMetaSteps (k + 1))
   const int first_run = t_begin >> 4, last_run = max((t_end - 1) >> 4, 0);
   auto gather = [&](int k) {
+    if (tid >= 4 * kMetaSteps) return;
     const int run = first_run + 4 * kMetaSteps * k + tid;
     int page = -1;
     float ks = 1.f, vs = 1.f;
@@ -537,47 +620,53 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   const int krow = 16 * ((x >> 2) & 1) + 4 * (x >> 3) + (x & 3);
   const int kkey = D == 128 ? ((krow & 3) | ((krow >> 4) & 1) << 2) : (((krow >> 1) & 1) | ((krow >> 4) & 1) << 1);
 
-  auto compute = [&](int i, auto wide_tag) {
-    constexpr bool WIDE = decltype(wide_tag)::value;
+  // One step.  PARTIAL: some row does not see some of its tokens.
+  auto compute = [&](int i, auto wide_tag, auto partial_tag) {
+    constexpr bool WIDE = decltype(wide_tag)::value, PARTIAL = decltype(partial_tag)::value;
     const int t0 = t_begin + i * kPrefillStep;
     const uint8_t* lk = ring[i % kPrefillSlots][0];
     const uint8_t* lv = ring[i % kPrefillSlots][1];
     const int mb = (i / kMetaSteps) & 1, mi = 4 * (i % kMetaSteps);
-    const int4 pages = *reinterpret_cast<const int4*>(&mpage[mb][mi]);
-    const bool gone_any = __builtin_amdgcn_readfirstlane(min(min(pages.x, pages.y), min(pages.z, pages.w))) < 0;
-    const bool partial = t0 + kPrefillStep > all_hi || t0 < all_lo || gone_any;
     f32x16 sc[2];
 #pragma unroll
-    for (int grp = 0; grp < 2; ++grp) {
+    for (int grp = 0; grp < 2; ++grp)
 #pragma unroll
       for (int k = 0; k < 16; ++k) sc[grp][k] = 0.f;
-      const float ks = F16 ? 1.0f : mks[mb][mi + 2 * grp + (krow >> 4)];
+    float kr[2];
 #pragma unroll
-      for (int u = 0; u < NP; ++u) {
+    for (int grp = 0; grp < 2; ++grp) kr[grp] = F16 ? 1.0f : mks[mb][mi + 2 * grp + (krow >> 4)];
+#pragma unroll
+    for (int u = 0; u < NP; ++u)
+#pragma unroll
+      for (int grp = 0; grp < 2; ++grp) {
         const uint4 c = *reinterpret_cast<const uint4*>(lk + (32 * grp + krow) * D + 16 * ((2 * u + h) ^ kkey));
         if constexpr (F16) {
-          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, ks), qf[2 * u], sc[grp], 0, 0, 0);
-          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, ks), qf[2 * u + 1], sc[grp], 0, 0, 0);
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, kr[grp]), qf[2 * u], sc[grp], 0, 0, 0);
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, kr[grp]), qf[2 * u + 1], sc[grp], 0, 0, 0);
         } else {
-          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16(c.x, c.y, ks), qf[2 * u], sc[grp], 0, 0, 0);
-          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16(c.z, c.w, ks), qf[2 * u + 1], sc[grp], 0, 0, 0);
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16(c.x, c.y, kr[grp]), qf[2 * u], sc[grp], 0, 0, 0);
+          sc[grp] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_bf16(c.z, c.w, kr[grp]), qf[2 * u + 1], sc[grp], 0, 0, 0);
         }
       }
-    }
+    uint32_t keep[2][4];
     float mx = -INFINITY;
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
-      if constexpr (F16) {  // the key scale of the lane's run of 16 tokens
+      if constexpr (F16) {
         const float ks = mks[mb][mi + 2 * grp + h];
 #pragma unroll
         for (int k = 0; k < 16; ++k) sc[grp][k] *= ks;
       }
-      if (partial) {
-        const int p = grp == 0 ? (h ? pages.y : pages.x) : (h ? pages.w : pages.z);
-        const int lo = p < 0 ? 0x7FFFFFFF : see_lo, t = t0 + 32 * grp + 16 * h;
+      if constexpr (PARTIAL) {
+        const bool none = mpage[mb][mi + 2 * grp + h] < 0;
+        const int t = t0 + 32 * grp + 16 * h, lo = none ? 0x7FFFFFFF : see_lo;
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           if (t + k < lo || t + k >= see_hi) sc[grp][k] = -INFINITY;
+        // what no row sees may hold anything, NaN codes too
+        const int vlo = none ? 0x7FFFFFFF : sp.lo;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) keep[grp][k] = token_bytes(t + 4 * k, vlo, t_end);
       }
 #pragma unroll
       for (int k = 0; k < 16; ++k) mx = fmaxf(mx, sc[grp][k]);
@@ -594,26 +683,17 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
         for (int k = 0; k < 16; ++k) o[d][k] *= al;
     }
     const float ms = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-#pragma unroll
-    for (int grp = 0; grp < 2; ++grp)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[grp][k], a.scale_log2, -ms));
-        sum += e;
-        sc[grp][k] = e;
-      }
-    l += sum;
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
       const float vs = mvs[mb][mi + 2 * grp + h];
-      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-      if (partial) {  // what no row sees may hold anything, NaN codes too
-        const int p = grp == 0 ? (h ? pages.y : pages.x) : (h ? pages.w : pages.z);
-        const int t = t0 + 32 * grp + 16 * h, lo = p < 0 ? 0x7FFFFFFF : sp.lo;
+      const uint8_t* vrow = lv + ((2 * grp + h) * D + x) * 16;
+      float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) keep[k] = token_bytes(t + 4 * k, lo, t_end);
+      for (int k = 0; k < 16; ++k) {
+        sc[grp][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[grp][k], a.scale_log2, -ms));
+        sum += sc[grp][k];
       }
+      l += sum;
       if constexpr (WIDE) {
         bf16x8 ph[2], pl[2];
 #pragma unroll
@@ -624,8 +704,8 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          uint4 c = *reinterpret_cast<const uint4*>(lv + ((2 * grp + h) * D + 32 * d + x) * 16);
-          c.x &= keep[0], c.y &= keep[1], c.z &= keep[2], c.w &= keep[3];
+          uint4 c = *reinterpret_cast<const uint4*>(vrow + 512 * d);
+          if constexpr (PARTIAL) c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
           const bf16x8 v0 = widen_bf16(c.x, c.y, vs), v1 = widen_bf16(c.z, c.w, vs);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, ph[0], o[d], 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, pl[0], o[d], 0, 0, 0);
@@ -638,8 +718,8 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
         for (int k = 0; k < 16; ++k) p[k >> 3][k & 7] = (_Float16)sc[grp][k];
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          uint4 c = *reinterpret_cast<const uint4*>(lv + ((2 * grp + h) * D + 32 * d + x) * 16);
-          if (partial) c.x &= keep[0], c.y &= keep[1], c.z &= keep[2], c.w &= keep[3];
+          uint4 c = *reinterpret_cast<const uint4*>(vrow + 512 * d);
+          if constexpr (PARTIAL) c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, vs), p[0], o[d], 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, vs), p[1], o[d], 0, 0, 0);
         }
@@ -647,21 +727,45 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
     }
   };
 
+  // Makes step i visible, and starts the copies of step i + 2.
+  auto advance = [&](int i) {
+    if (i + 1 < steps)
+      wait_copies<CPW>();
+    else
+      wait_copies<0>();
+    __syncthreads();  // step i is in LDS, and nobody reads step i - 1 any more
+    if (i % kMetaSteps == kMetaSteps / 2 && i + kMetaSteps / 2 < steps) gather(i / kMetaSteps + 1);
+    if (i + 2 < steps) issue(i + 2);
+  };
+  // Steps of which this wavefront's rows see everything are a loop of their own,
+  // between two that mask (one loop that picks the variant step by step moved the
+  // accumulator between registers every time).
   auto walk = [&](auto wide_tag) {
+    auto masked = [&](int from, int to) {
+      for (int i = from; i < to; ++i) {
+        advance(i);
+        const int t0 = t_begin + i * kPrefillStep;
+        if (t0 < w_hi && t0 + kPrefillStep > w_lo) compute(i, wide_tag, std::true_type{});
+      }
+    };
     gather(0);
     __syncthreads();
     issue(0);
     if (steps > 1) issue(1);
-    for (int i = 0; i < steps; ++i) {
-      if (i + 1 < steps)
-        wait_copies<CPW>();
-      else
-        wait_copies<0>();
-      __syncthreads();  // step i is in LDS, and nobody reads step i - 1 any more
-      if (i % kMetaSteps == kMetaSteps / 2 && i + kMetaSteps / 2 < steps) gather(i / kMetaSteps + 1);
-      if (i + 2 < steps) issue(i + 2);
-      const int t0 = t_begin + i * kPrefillStep;
-      if (t0 < w_hi && t0 + kPrefillStep > w_lo) compute(i, wide_tag);
+    if constexpr (decltype(wide_tag)::value) {
+      masked(0, steps);
+    } else {
+      int from = steps, to = steps;  // with missing blocks every step is masked
+      if (!missing) {
+        from = min(max((all_lo - t_begin + kPrefillStep - 1) / kPrefillStep, 0), steps);
+        to = min(max((all_hi - t_begin) / kPrefillStep, from), steps);
+      }
+      masked(0, from);
+      for (int i = from; i < to; ++i) {
+        advance(i);
+        compute(i, wide_tag, std::false_type{});
+      }
+      masked(to, steps);
     }
   };
   if (steps > 0) {
@@ -705,12 +809,17 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Joins the splits of a row: one wavefront per row, splits in ascending order.
+// Joins the splits of a row: one workgroup per row.  D / 4 threads take the row's
+// channels, four each, of every (1024 / D)th split, keeping a running maximum as
+// the attention itself does; the groups are joined in LDS in ascending order.
+// Four splits are read at a time: with one, the join of 64 splits took longer
+// than the attention (the loads' latency, one after the other).
 template <bool F16, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_rows) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int TPG = D / 4, NG = 256 / TPG, U = 4;
+  __shared__ f32x4 so[NG][TPG];
+  __shared__ float sm[NG], sl[NG];
+  const int64_t id = workgroup_id();
   if (id >= (int64_t)a.kb.T * a.Hq) return;
   const int t = (int)(id / a.Hq), head = (int)(id - (int64_t)t * a.Hq);
   int64_t f0;
@@ -722,22 +831,61 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_r
   const int r = (t - s.c0) * a.G + head % a.G, r0 = r / tile * tile;
   const int ns = row_span(a, s, r0, min(r0 + tile, rows)).splits;
   if (ns <= 1) return;  // written already
+  const int g = threadIdx.x / TPG, c = threadIdx.x % TPG;
   const int64_t step = (int64_t)a.kb.T * a.Hq;
-  float mm = -INFINITY;
-  for (int i = 0; i < ns; ++i) mm = fmaxf(mm, a.part_ml[2 * (id + i * step)]);
-  const float ms = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f, acc[E] = {};
-  for (int i = 0; i < ns; ++i) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (id + i * step));
-    const float f = __builtin_amdgcn_exp2f(ml.x - ms);
-    ll = __builtin_fmaf(ml.y, f, ll);
+  float m = -INFINITY, l = 0.f;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = g; i0 < ns; i0 += NG * U) {
+    float2 ml[U];
+    f32x4 o[U];
+    float mn = m;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = __builtin_fmaf(a.part_o[(id + i * step) * D + lane * E + e], f, acc[e]);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * NG;
+      const int64_t at = id + min(i, ns - 1) * step;
+      ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+      o[u] = *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * c);
+      if (i >= ns) ml[u] = make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+    const float ms = mn == -INFINITY ? 0.f : mn;
+    const float al = __builtin_amdgcn_exp2f(m - ms);
+    m = mn;
+    l *= al;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] *= al;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = __builtin_amdgcn_exp2f(ml[u].x - ms);
+      if (i0 + u * NG >= ns) continue;
+      l = __builtin_fmaf(ml[u].y, f, l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(o[u][e], f, acc[e]);
+    }
+  }
+  so[g][c] = acc;
+  if (c == 0) sm[g] = m, sl[g] = l;
+  __syncthreads();
+  if (g > 0) return;
+  float mm = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < NG; ++k) mm = fmaxf(mm, sm[k]);
+  const float ms = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f;
+  acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    const float f = __builtin_amdgcn_exp2f(sm[k] - ms);
+    ll = __builtin_fmaf(sl[k], f, ll);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(so[k][c][e], f, acc[e]);
   }
   const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) a.out[(int64_t)t * a.ld_o + head * D + lane * E + e] = round16<F16>(acc[e] * inv);
-  if (a.lse && lane == 0) a.lse[id] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+  const uint32_t u0 = (uint32_t)round16<F16>(acc[0] * inv) | (uint32_t)round16<F16>(acc[1] * inv) << 16;
+  const uint32_t u1 = (uint32_t)round16<F16>(acc[2] * inv) | (uint32_t)round16<F16>(acc[3] * inv) << 16;
+  *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.ld_o + head * D + 4 * c) = make_uint2(u0, u1);
+  if (a.lse && c == 0) a.lse[id] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -756,12 +904,17 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
   if (!p.prefill) p.row_limit = 0x7FFFFFFF;
   else if (B * max_q == T) p.row_limit = p.decode_tiles = 0;  // no short ones, by what we are told
   else p.row_limit = 64;
+  // Chunks: long enough that a workgroup's start (about 4 us of dependent reads)
+  // is small beside its stream, short enough that ragged lengths spread over the
+  // chip and that 512 workgroups, two a CU, exist.  64 sequences of 500 .. 16384
+  // tokens, 8 heads: 203 us with chunks of 2048, 209 with 4096, 240 with 8192; 2 of
+  // 131072 with 32 rows: 99 us with 4096, 114 with 2048, 132 with 1024.
   const int64_t tile = p.prefill ? kPrefillRows : 16 * p.decode_tiles;
   const int64_t tiles = std::max<int64_t>(1, std::max<int64_t>(T * G / tile, std::min(B, T))) * Hkv;
-  const int64_t want = p.prefill ? 512 : 1024;
   const int64_t unit = p.prefill ? 512 : 256;
-  int64_t ns = std::max<int64_t>(1, want / tiles);
-  int64_t chunk = (max_kv + ns - 1) / ns;
+  const int64_t most = p.prefill ? max_kv : p.decode_tiles == 1 ? 2048 : 4096;
+  const int64_t ns = std::max<int64_t>(1, 512 / tiles);
+  int64_t chunk = std::min((max_kv + ns - 1) / ns, most);
   chunk = std::max<int64_t>(unit, (chunk + unit - 1) / unit * unit);
   p.chunk = (int)chunk;
   p.nsplit = (int)std::max<int64_t>(1, (max_kv + chunk - 1) / chunk);
@@ -771,19 +924,14 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
 template <bool F16, int D>
 static void attn_launch(AttnArgs a, const AttnPlan& p, hipStream_t s) {
   const int64_t R = (int64_t)a.kb.T * a.G;
-  if (p.prefill) {
-    const dim3 grid((uint32_t)(R / kPrefillRows + a.kb.B), a.c.heads, p.nsplit);
-    attn_prefill_kernel<F16, D><<<grid, 256, 0, s>>>(a);
-  }
-  if (p.decode_tiles == 1) {
-    const dim3 grid((uint32_t)(R / 16 + a.kb.B), a.c.heads, p.nsplit);
-    attn_decode_kernel<F16, D, 1><<<grid, 256, 0, s>>>(a);
-  } else if (p.decode_tiles == 2) {
-    const dim3 grid((uint32_t)(R / 32 + a.kb.B), a.c.heads, p.nsplit);
-    attn_decode_kernel<F16, D, 2><<<grid, 256, 0, s>>>(a);
-  }
+  if (p.prefill)
+    attn_prefill_kernel<F16, D><<<grid_of(prefill_slots(a) * a.c.heads * a.nsplit), 256, 0, s>>>(a);
+  if (p.decode_tiles == 1)
+    attn_decode_kernel<F16, D, 1><<<grid_of((R / 16 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
+  else if (p.decode_tiles == 2)
+    attn_decode_kernel<F16, D, 2><<<grid_of((R / 32 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
   if (p.nsplit > 1)
-    attn_join_kernel<F16, D><<<(uint32_t)(((int64_t)a.kb.T * a.Hq + 3) / 4), 256, 0, s>>>(a, 16 * p.decode_tiles);
+    attn_join_kernel<F16, D><<<grid_of((int64_t)a.kb.T * a.Hq), 256, 0, s>>>(a, 16 * p.decode_tiles);
 }
 
 hipError_t launch_attention(const AttnArgs& a, bool f16, const AttnPlan& p, hipStream_t s) {

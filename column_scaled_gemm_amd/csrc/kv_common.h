@@ -12,13 +12,15 @@ struct Seq {
 };
 
 // The device arrays are data, not checked by the host: whatever they hold, the
-// rows lie in [0, T) and the length within the block table's reach.
+// rows lie in [0, T) and the length within the block table's reach.  b is
+// wavefront-uniform, and so is the result, in scalar registers: what is decided
+// from it is a scalar branch.
 __device__ __forceinline__ Seq load_seq(const KvBatch& kb, int b, int block_shift) {
   Seq s;
   const int T = kb.T;
-  s.c0 = min(max(kb.cu[b], 0), T);
-  s.n = min(max(kb.cu[b + 1], s.c0), T) - s.c0;
-  s.len = min(max(kb.lens[b], 0), kb.max_blocks << block_shift);
+  s.c0 = min(max(__builtin_amdgcn_readfirstlane(kb.cu[b]), 0), T);
+  s.n = min(max(__builtin_amdgcn_readfirstlane(kb.cu[b + 1]), s.c0), T) - s.c0;
+  s.len = min(max(__builtin_amdgcn_readfirstlane(kb.lens[b]), 0), kb.max_blocks << block_shift);
   return s;
 }
 
@@ -48,7 +50,8 @@ __device__ __forceinline__ int find_seq(const KvBatch& kb, int64_t u, int mul, i
     span = min(step, span - k * step);
     if (step == 1) break;
   }
-  *first = f0;
+  *first = (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(f0 >> 32)) << 32) |
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)f0));
   return __builtin_amdgcn_readfirstlane(lo);
 }
 

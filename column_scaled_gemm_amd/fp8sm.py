@@ -112,9 +112,16 @@ def _check(status, where):
         raise Fp8smError(status, where)
 
 
+# The raw handle of the current stream without building a Stream object (3 us of
+# host time a call, measured), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _ptr(t):
@@ -123,14 +130,29 @@ def _ptr(t):
     another device than the current one, is refused here, before the library
     is called."""
     if t is None:
-        return ctypes.c_void_p(0)
-    if not t.is_cuda:
+        return None
+    d = t.get_device()
+    if d < 0:
         raise DeviceTensorError("tensor arguments must be device (cuda) tensors; got one on "
                                 f"{t.device}")
-    if t.device.index != torch.cuda.current_device():
+    if d != torch.cuda.current_device():
         raise DeviceTensorError(f"tensor on {t.device}, but the current device is "
                                 f"cuda:{torch.cuda.current_device()}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _ptrs(*tensors):
+    """_ptr of each of several tensors, asking for the current device once."""
+    cur = torch.cuda.current_device() if tensors[0].is_cuda else None
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif t.get_device() == cur:
+            out.append(t.data_ptr())
+        else:
+            out.append(_ptr(t))
+    return out
 
 
 def _dtype_code(t):
@@ -663,11 +685,11 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_
     for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None:
             _holds_bytes(t, 2 * head_dim, what, x.dtype)
-    st = _load().fp8sm_qk_norm_rope(_ptr(x), _dtype_code(x), T, q_heads, k_heads, head_dim,
-                                    _row_ld(x), _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin),
-                                    max_pos, _ptr(positions), rot,
-                                    ROPE_INTERLEAVED if interleaved else 0, _ptr(out),
-                                    _row_ld(out), _stream(stream))
+    px, pq, pk, pc, pp, po = _ptrs(x, q_weight, k_weight, cos_sin, positions, out)
+    st = _load().fp8sm_qk_norm_rope(px, _dtype_code(x), T, q_heads, k_heads, head_dim, _row_ld(x),
+                                    pq, pk, eps, pc, max_pos, pp, rot,
+                                    ROPE_INTERLEAVED if interleaved else 0, po, _row_ld(out),
+                                    _stream(stream))
     _check(st, "fp8sm_qk_norm_rope")
     return out
 
@@ -699,31 +721,32 @@ def kv_cache_empty(num_blocks, heads, head_dim, block, device="cuda"):
 def _cache_args(cache):
     """(blocks, heads, D, block) of a cache whose four tensors agree."""
     k, v, ke, ve = cache
-    if k.dim() != 4:
-        raise ValueError(f"cache.k: needs [blocks, heads, block, D], got {tuple(k.shape)}")
-    P, H, block, D = k.shape
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"cache.k: needs [blocks, heads, block, D], got {tuple(shape)}")
+    P, H, block, D = shape
     if v.shape != (P, H, block // 16, D, 16) or ke.shape != (P, H) or ve.shape != (P, H):
         raise ValueError(f"cache: v {tuple(v.shape)}, k_exp {tuple(ke.shape)}, v_exp {tuple(ve.shape)} "
-                         f"do not go with k {tuple(k.shape)}")
-    for t in cache:
-        if t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError("cache: needs contiguous uint8 tensors")
+                         f"do not go with k {tuple(shape)}")
+    u8 = torch.uint8
+    if k.dtype != u8 or v.dtype != u8 or ke.dtype != u8 or ve.dtype != u8 or not (
+            k.is_contiguous() and v.is_contiguous() and ke.is_contiguous() and ve.is_contiguous()):
+        raise ValueError("cache: needs contiguous uint8 tensors")
     return P, H, D, block
 
 
 def _batch_args(cu, lens, table):
     """(sequences, table row stride, blocks a sequence) of a ragged batch."""
-    B = lens.shape[0]
-    if cu.dtype != torch.int32 or lens.dtype != torch.int32 or table.dtype != torch.int32:
+    i32 = torch.int32
+    if cu.dtype != i32 or lens.dtype != i32 or table.dtype != i32:
         raise TypeError("cu, lens and table must be int32")
-    if cu.dim() != 1 or lens.dim() != 1 or cu.shape[0] != B + 1 or table.dim() != 2 or \
-            table.shape[0] != B:
+    B, shape = lens.numel(), table.shape
+    if cu.shape != (B + 1,) or lens.dim() != 1 or len(shape) != 2 or shape[0] != B:
         raise ValueError(f"cu {tuple(cu.shape)}, lens {tuple(lens.shape)}, table {tuple(table.shape)}: "
                          "need [B + 1], [B], [B, blocks]")
-    if not cu.is_contiguous() or not lens.is_contiguous() or \
-            (table.shape[1] > 1 and table.stride(1) != 1):
+    n = shape[1]
+    if not cu.is_contiguous() or not lens.is_contiguous() or (n > 1 and table.stride(1) != 1):
         raise ValueError("cu, lens and the rows of table must be contiguous")
-    n = table.shape[1]
     return B, (table.stride(0) if B > 1 else n), n
 
 
@@ -738,10 +761,9 @@ def kv_cache_write(k, v, cache, cu, lens, table, stream=None):
     Tv, ld_v = _head_rows(v, H, D, "v")
     if Tv != T or v.dtype != k.dtype:
         raise ValueError("k and v must have the same rows and dtype")
-    st = _load().fp8sm_kv_cache_write(
-        _ptr(k), ld_k, _ptr(v), ld_v, _dtype_code(k), T, B, _ptr(cu), _ptr(lens), _ptr(table),
-        ld_table, n, P, H, D, block, _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
-        _ptr(cache[3]), _stream(stream))
+    pk, pv, pc, pl, pt, *codes = _ptrs(k, v, cu, lens, table, *cache)
+    st = _load().fp8sm_kv_cache_write(pk, ld_k, pv, ld_v, _dtype_code(k), T, B, pc, pl, pt, ld_table,
+                                      n, P, H, D, block, *codes, _stream(stream))
     _check(st, "fp8sm_kv_cache_write")
     return cache
 
@@ -760,10 +782,9 @@ def kv_cache_read(cache, cu, lens, table, total, dtype=torch.bfloat16, k=None, v
     Tv, ld_v = _head_rows(v, H, D, "v")
     if Tk < total or Tv < total or k.dtype != dtype or v.dtype != dtype:
         raise ValueError(f"k and v need {total} rows of {dtype}")
-    st = _load().fp8sm_kv_cache_read(
-        _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]), _ptr(cache[3]), P, H, D, block, total, B,
-        _ptr(cu), _ptr(lens), _ptr(table), ld_table, n, _dtype_code(k), _ptr(k), ld_k, _ptr(v),
-        ld_v, _stream(stream))
+    pk, pv, pc, pl, pt, *codes = _ptrs(k, v, cu, lens, table, *cache)
+    st = _load().fp8sm_kv_cache_read(*codes, P, H, D, block, total, B, pc, pl, pt, ld_table, n,
+                                     _dtype_code(k), pk, ld_k, pv, ld_v, _stream(stream))
     _check(st, "fp8sm_kv_cache_read")
     return k, v
 
@@ -809,10 +830,10 @@ def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, c
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         if stream is not None:
             workspace.record_stream(stream)
+    pq, pc, pl, pt, po, pe, pw, *codes = _ptrs(q, cu, lens, table, out, lse, workspace, *cache)
     st = L.fp8sm_attention_cache(
-        _ptr(q), ld_q, _dtype_code(q), T, B, Hq, _ptr(cu), _ptr(lens), _ptr(table), ld_table, n,
-        _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]), _ptr(cache[3]), P, H, D, block, max_q,
-        max_kv, D ** -0.5 if scale is None else scale, ATTN_CAUSAL if causal else 0, window,
-        _ptr(out), ld_o, _ptr(lse), _ptr(workspace), need, _stream(stream))
+        pq, ld_q, _dtype_code(q), T, B, Hq, pc, pl, pt, ld_table, n, *codes, P, H, D, block, max_q,
+        max_kv, D ** -0.5 if scale is None else scale, ATTN_CAUSAL if causal else 0, window, po,
+        ld_o, pe, pw, need, _stream(stream))
     _check(st, "fp8sm_attention_cache")
     return (out, lse) if return_lse else out

@@ -335,7 +335,7 @@ fp8sm_status fp8sm_silu_mul_f32(const void* x, fp8sm_dtype in, int64_t M, int64_
  * Codes 16-byte aligned.  block is 16, 32, 64 or 128; D is 64 or 128.
  * Common errors: T, nseq < 0, heads < 1, num_blocks < 1, max_blocks < 1, ld
  * below a row's length, ld_table < max_blocks -> ERR_SHAPE; D or block not
- * listed -> ERR_UNSUPPORTED; T > 2^24, nseq > 2^20, heads > 1024, num_blocks >
+ * listed -> ERR_UNSUPPORTED; T > 2^23, nseq > 2^20, heads > 1024, num_blocks >
  * 2^31 - 1, max_blocks * block > 2^30 -> ERR_RANGE; alignment -> ERR_ALIGN.
  * T == 0 or nseq == 0 launches nothing.
  */
