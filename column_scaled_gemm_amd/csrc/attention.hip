@@ -809,77 +809,81 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Joins the splits of a row: one workgroup per row.  D / 4 threads take the row's
-// channels, four each, of every (1024 / D)th split, keeping a running maximum as
-// the attention itself does; the groups are joined in LDS in ascending order.
-// Four splits are read at a time: with one, the join of 64 splits took longer
-// than the attention (the loads' latency, one after the other).
-template <bool F16, int D>
+// Joins the splits of a row, WPR wavefronts per row: four for many splits, one
+// for few.  D / 4 lanes take the row's channels, four each, of every NG-th split,
+// keeping a running maximum as the attention itself does; the groups are joined
+// in ascending order.  Four splits are read at a time: with one, the join of 64
+// splits took longer than the attention (the loads' latency, one after the
+// other).
+template <bool F16, int D, int WPR>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_rows) {
-  constexpr int TPG = D / 4, NG = 256 / TPG, U = 4;
-  __shared__ f32x4 so[NG][TPG];
-  __shared__ float sm[NG], sl[NG];
-  const int64_t id = workgroup_id();
-  if (id >= (int64_t)a.kb.T * a.Hq) return;
-  const int t = (int)(id / a.Hq), head = (int)(id - (int64_t)t * a.Hq);
+  constexpr int TPG = D / 4, NG = WPR * 64 / TPG, U = 4;
+  __shared__ f32x4 so[256 / TPG][TPG];
+  __shared__ float sm[256 / TPG], sl[256 / TPG];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = workgroup_id() * (4 / WPR) + wave / WPR;
+  const bool there = id < (int64_t)a.kb.T * a.Hq;
+  const int t = there ? (int)(id / a.Hq) : 0, head = there ? (int)(id - (int64_t)t * a.Hq) : 0;
   int64_t f0;
   const int b = find_seq(a.kb, t, 1, 0, 0, &f0);
   const Seq s = load_seq(a.kb, b, a.c.block_shift);
-  if (t < s.c0 || t >= s.c0 + s.n) return;  // no sequence's row
   const int rows = s.n * a.G;
   const int tile = rows > a.row_limit ? kPrefillRows : decode_rows;
   const int r = (t - s.c0) * a.G + head % a.G, r0 = r / tile * tile;
-  const int ns = row_span(a, s, r0, min(r0 + tile, rows)).splits;
-  if (ns <= 1) return;  // written already
-  const int g = threadIdx.x / TPG, c = threadIdx.x % TPG;
+  int ns = 0;
+  if (there && t >= s.c0 && t < s.c0 + s.n)  // some sequence's row
+    ns = row_span(a, s, r0, min(r0 + tile, rows)).splits;
+  const int gw = threadIdx.x / TPG, g = gw % NG, c = threadIdx.x % TPG;
   const int64_t step = (int64_t)a.kb.T * a.Hq;
   float m = -INFINITY, l = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = g; i0 < ns; i0 += NG * U) {
-    float2 ml[U];
-    f32x4 o[U];
-    float mn = m;
+  if (ns > 1) {  // (with one split the row is written already)
+    for (int i0 = g; i0 < ns; i0 += NG * U) {
+      float2 ml[U];
+      f32x4 o[U];
+      float mn = m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * NG;
-      const int64_t at = id + min(i, ns - 1) * step;
-      ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
-      o[u] = *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * c);
-      if (i >= ns) ml[u] = make_float2(-INFINITY, 0.f);
-    }
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * NG;
+        const int64_t at = id + min(i, ns - 1) * step;
+        ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+        o[u] = *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * c);
+        if (i >= ns) ml[u] = make_float2(-INFINITY, 0.f);
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    const float al = __builtin_amdgcn_exp2f(m - ms);
-    m = mn;
-    l *= al;
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
+      const float ms = mn == -INFINITY ? 0.f : mn;
+      const float al = __builtin_amdgcn_exp2f(m - ms);
+      m = mn;
+      l *= al;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] *= al;
+      for (int e = 0; e < 4; ++e) acc[e] *= al;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float f = __builtin_amdgcn_exp2f(ml[u].x - ms);
-      if (i0 + u * NG >= ns) continue;
-      l = __builtin_fmaf(ml[u].y, f, l);
+      for (int u = 0; u < U; ++u) {
+        const float f = __builtin_amdgcn_exp2f(ml[u].x - ms);
+        if (i0 + u * NG >= ns) continue;
+        l = __builtin_fmaf(ml[u].y, f, l);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(o[u][e], f, acc[e]);
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(o[u][e], f, acc[e]);
+      }
     }
   }
-  so[g][c] = acc;
-  if (c == 0) sm[g] = m, sl[g] = l;
+  so[gw][c] = acc;
+  if (c == 0) sm[gw] = m, sl[gw] = l;
   __syncthreads();
-  if (g > 0) return;
+  if (ns <= 1 || g > 0) return;
   float mm = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < NG; ++k) mm = fmaxf(mm, sm[k]);
+  for (int k = 0; k < NG; ++k) mm = fmaxf(mm, sm[gw + k]);
   const float ms = mm == -INFINITY ? 0.f : mm;
   float ll = 0.f;
   acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    const float f = __builtin_amdgcn_exp2f(sm[k] - ms);
-    ll = __builtin_fmaf(sl[k], f, ll);
+    const float f = __builtin_amdgcn_exp2f(sm[gw + k] - ms);
+    ll = __builtin_fmaf(sl[gw + k], f, ll);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(so[k][c][e], f, acc[e]);
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(so[gw + k][c][e], f, acc[e]);
   }
   const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
   const uint32_t u0 = (uint32_t)round16<F16>(acc[0] * inv) | (uint32_t)round16<F16>(acc[1] * inv) << 16;
@@ -930,8 +934,11 @@ static void attn_launch(AttnArgs a, const AttnPlan& p, hipStream_t s) {
     attn_decode_kernel<F16, D, 1><<<grid_of((R / 16 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
   else if (p.decode_tiles == 2)
     attn_decode_kernel<F16, D, 2><<<grid_of((R / 32 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
-  if (p.nsplit > 1)
-    attn_join_kernel<F16, D><<<grid_of((int64_t)a.kb.T * a.Hq), 256, 0, s>>>(a, 16 * p.decode_tiles);
+  const int64_t out_rows = (int64_t)a.kb.T * a.Hq;
+  if (p.nsplit > 8)
+    attn_join_kernel<F16, D, 4><<<grid_of(out_rows), 256, 0, s>>>(a, 16 * p.decode_tiles);
+  else if (p.nsplit > 1)
+    attn_join_kernel<F16, D, 1><<<grid_of((out_rows + 3) / 4), 256, 0, s>>>(a, 16 * p.decode_tiles);
 }
 
 hipError_t launch_attention(const AttnArgs& a, bool f16, const AttnPlan& p, hipStream_t s) {
