@@ -598,14 +598,10 @@ static bool attention_sizes(int64_t T, int64_t nseq, int32_t Hq, int32_t Hkv, in
          max_q >= 1 && max_kv >= 0;
 }
 
-static size_t attention_bytes(int64_t T, int32_t Hq, int32_t D, const AttnPlan& p) {
-  return p.nsplit > 1 ? (size_t)p.nsplit * T * Hq * (D + 2) * sizeof(float) : 0;
-}
-
 size_t fp8sm_attention_cache_workspace(int64_t T, int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
-                                       int64_t max_q, int64_t max_kv) {
-  if (!attention_sizes(T, nseq, Hq, Hkv, D, max_q, max_kv)) return 0;
-  return attention_bytes(T, Hq, D, plan_attention(T, nseq, Hq, Hkv, D, max_q, max_kv));
+                                       int64_t max_q, int64_t max_kv, int32_t window) {
+  if (!attention_sizes(T, nseq, Hq, Hkv, D, max_q, max_kv) || window < 0) return 0;
+  return plan_attention(T, nseq, Hq, Hkv, D, max_q, max_kv, window).bytes();
 }
 
 fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, int64_t T,
@@ -633,8 +629,8 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   if (T == 0 || nseq == 0) return FP8SM_OK;
   if (!q || !o) return FP8SM_ERR_NULL;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return FP8SM_ERR_ALIGN;
-  const AttnPlan p = plan_attention(T, nseq, Hq, Hkv, D, max_q, max_kv);
-  const size_t need = attention_bytes(T, Hq, D, p);
+  const AttnPlan p = plan_attention(T, nseq, Hq, Hkv, D, max_q, max_kv, window);
+  const size_t need = p.bytes();
   if (need > 0 && !workspace) return FP8SM_ERR_NULL;
   if (workspace_bytes < need) return FP8SM_ERR_SHAPE;
   if (!aligned(workspace, 16)) return FP8SM_ERR_ALIGN;
@@ -652,10 +648,14 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   a.negate = scale < 0.f;
   a.causal = (flags & FP8SM_ATTN_CAUSAL) != 0;
   a.window = window;
-  a.nsplit = p.nsplit;
-  a.chunk = p.chunk;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = a.part_o + (need ? (size_t)p.nsplit * T * Hq * D : 0);
+  auto place = [&](AttnSplit sp, size_t offset) {
+    sp.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + offset);
+    sp.ml = sp.n > 1 ? sp.o + (size_t)sp.n * sp.rows * D : sp.o;
+    return sp;
+  };
+  a.few = place(p.few_split, 0);
+  a.many = place(p.many_split, p.offset_many());
+  a.few_by_seq = p.few_by_seq;
   a.row_limit = p.row_limit;
   return launched(launch_attention(a, in == FP8SM_FP16, p, stream));
 }

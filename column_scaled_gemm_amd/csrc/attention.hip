@@ -70,7 +70,7 @@ struct Span {
   int lo, hi, start;
   int chunk, splits;  // tokens of a split, splits in use
 };
-__device__ __forceinline__ Span row_span(const AttnArgs& a, const Seq& s, int r0, int r1) {
+__device__ __forceinline__ Span row_span(const AttnArgs& a, const AttnSplit& sp, const Seq& s, int r0, int r1) {
   const int first = s.len - s.n + r0 / a.G, last = s.len - s.n + (r1 - 1) / a.G;
   Span p;
   p.hi = a.causal ? max(min(s.len, last + 1), 0) : s.len;
@@ -78,9 +78,13 @@ __device__ __forceinline__ Span row_span(const AttnArgs& a, const Seq& s, int r0
   p.start = p.lo & ~63;
   // the plan's chunk, longer where the lengths go beyond what the plan was told
   const int span = max(p.hi - p.start, 0);
-  p.chunk = max(a.chunk, ((span + a.nsplit - 1) / a.nsplit + 63) & ~63);
+  p.chunk = max(sp.chunk, ((span + sp.n - 1) / sp.n + 63) & ~63);
   p.splits = (span + p.chunk - 1) / p.chunk;
   return p;
+}
+// A row's place among the unjoined rows of a split.
+__device__ __forceinline__ int64_t part_row(const AttnArgs& a, bool few, int b, int r, int64_t t, int head) {
+  return few && a.few_by_seq ? ((int64_t)b * kFewRows + r) * a.c.heads + head / a.G : t * a.Hq + head;
 }
 
 // Grids are one list of workgroups; more than a grid's first dimension takes
@@ -114,7 +118,7 @@ __device__ __forceinline__ float quarter_max(float v) {
 // scores of the consecutive tokens 16 g .. 16 g + 15.
 constexpr int kDecodeRuns = 256;  // runs of 16 tokens a gather brings
 
-__host__ __device__ __forceinline__ int decode_stride(const AttnArgs& a) { return a.c.heads * a.nsplit | 1; }
+__host__ __device__ __forceinline__ int decode_stride(const AttnArgs& a) { return a.c.heads * a.few.n | 1; }
 
 template <bool F16, int D, int QT>
 __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
@@ -131,7 +135,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
   // even one, 154 us where 106 were due).
   const int per = decode_stride(a), id = (int)(workgroup_id() % per);
   const int64_t slot = workgroup_id() / per;
-  if (id >= a.c.heads * a.nsplit) return;
+  if (id >= a.c.heads * a.few.n) return;
   const int hk = id % a.c.heads, split = id / a.c.heads;
   int64_t f0;
   const int b = find_seq(a.kb, slot, a.G, QT == 2 ? 5 : 4, 1, &f0);
@@ -140,7 +144,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
   const int64_t r64 = (slot - f0) * (16 * QT);
   if (r64 >= rows || rows > a.row_limit) return;
   const int r0 = (int)r64;
-  const Span sp = row_span(a, s, r0, min(r0 + 16 * QT, rows));
+  const Span sp = row_span(a, a.few, s, r0, min(r0 + 16 * QT, rows));
   const int ns = sp.splits;
   if (split >= max(ns, 1)) return;
   const int t_begin = sp.start + split * sp.chunk;
@@ -406,11 +410,11 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
       *reinterpret_cast<uint4*>(a.out + t * a.ld_o + head * D + d) = make_uint4(u[0], u[1], u[2], u[3]);
       if (a.lse && d == 0) a.lse[t * a.Hq + head] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
     } else {
-      const int64_t at = ((int64_t)split * a.kb.T + t) * a.Hq + head;
-      float* po = a.part_o + at * D + d;
+      const int64_t at = split * a.few.rows + part_row(a, true, b, r, t, head);
+      float* po = a.few.o + at * D + d;
       *reinterpret_cast<f32x4*>(po) = f32x4{acc[0], acc[1], acc[2], acc[3]};
       *reinterpret_cast<f32x4*>(po + 4) = f32x4{acc[4], acc[5], acc[6], acc[7]};
-      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(mm, ll);
+      if (d == 0) *reinterpret_cast<float2*>(a.few.ml + 2 * at) = make_float2(mm, ll);
     }
   }
 }
@@ -478,14 +482,14 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   // with more work, each takes a contiguous part of the list, so that the tiles
   // that read the same keys share an L2 (8320 tokens, 56 heads: 1237 us in
   // list order, 1147 so; tiles in ascending order 1197).
-  const int64_t slots = prefill_slots(a), n = slots * a.c.heads * a.nsplit, id = workgroup_id();
+  const int64_t slots = prefill_slots(a), n = slots * a.c.heads * a.many.n, id = workgroup_id();
   if (id >= n) return;
-  const int pairs = a.c.heads * a.nsplit;
+  const int pairs = a.c.heads * a.many.n;
   const int64_t part = n >> 3, rest = n & 7;
   const int64_t at = pairs % 8 == 0 || pairs >= 64 ? (id & 7) * part + min(id & 7, rest) + (id >> 3) : id;
   const int64_t pair = at / slots, k = at - pair * slots;
   const int64_t slot = slots - 1 - k;
-  const int hk = (int)(pair / a.nsplit), split = (int)(pair - (int64_t)hk * a.nsplit);
+  const int hk = (int)(pair / a.many.n), split = (int)(pair - (int64_t)hk * a.many.n);
   int64_t f0;
   const int b = find_seq(a.kb, slot, a.G, 7, 1, &f0);
   const Seq s = load_seq(a.kb, b, bs);
@@ -493,7 +497,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   const int64_t r64 = (slot - f0) * kPrefillRows;
   if (r64 >= rows || rows <= a.row_limit) return;
   const int r0 = (int)r64;
-  const Span sp = row_span(a, s, r0, min(r0 + kPrefillRows, rows));
+  const Span sp = row_span(a, a.many, s, r0, min(r0 + kPrefillRows, rows));
   const int ns = sp.splits;
   if (split >= max(ns, 1)) return;
   const int t_begin = sp.start + split * sp.chunk;
@@ -797,14 +801,14 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
       }
     if (a.lse && h == 0) a.lse[t * a.Hq + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
   } else {
-    const int64_t at = ((int64_t)split * a.kb.T + t) * a.Hq + head;
+    const int64_t at = split * a.many.rows + part_row(a, false, b, r, t, head);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        *reinterpret_cast<f32x4*>(a.part_o + at * D + 32 * d + 8 * v + 4 * h) =
+        *reinterpret_cast<f32x4*>(a.many.o + at * D + 32 * d + 8 * v + 4 * h) =
             f32x4{o[d][4 * v] * vref, o[d][4 * v + 1] * vref, o[d][4 * v + 2] * vref, o[d][4 * v + 3] * vref};
-    if (h == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(m, l);
+    if (h == 0) *reinterpret_cast<float2*>(a.many.ml + 2 * at) = make_float2(m, l);
   }
 }
 
@@ -816,7 +820,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
 // splits took longer than the attention (the loads' latency, one after the
 // other).
 template <bool F16, int D, int WPR>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_rows) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int few_rows) {
   constexpr int TPG = D / 4, NG = WPR * 64 / TPG, U = 4;
   __shared__ f32x4 so[256 / TPG][TPG];
   __shared__ float sm[256 / TPG], sl[256 / TPG];
@@ -828,13 +832,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_r
   const int b = find_seq(a.kb, t, 1, 0, 0, &f0);
   const Seq s = load_seq(a.kb, b, a.c.block_shift);
   const int rows = s.n * a.G;
-  const int tile = rows > a.row_limit ? kPrefillRows : decode_rows;
+  const bool few = rows <= a.row_limit;
+  const AttnSplit& sp = few ? a.few : a.many;
+  const int tile = few ? few_rows : kPrefillRows;
   const int r = (t - s.c0) * a.G + head % a.G, r0 = r / tile * tile;
   int ns = 0;
   if (there && t >= s.c0 && t < s.c0 + s.n)  // some sequence's row
-    ns = row_span(a, s, r0, min(r0 + tile, rows)).splits;
+    ns = row_span(a, sp, s, r0, min(r0 + tile, rows)).splits;
   const int gw = threadIdx.x / TPG, g = gw % NG, c = threadIdx.x % TPG;
-  const int64_t step = (int64_t)a.kb.T * a.Hq;
+  const int64_t part = part_row(a, few, b, r, t, head);
   float m = -INFINITY, l = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   if (ns > 1) {  // (with one split the row is written already)
@@ -845,9 +851,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_r
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * NG;
-        const int64_t at = id + min(i, ns - 1) * step;
-        ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
-        o[u] = *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * c);
+        const int64_t at = part + min(i, ns - 1) * sp.rows;
+        ml[u] = *reinterpret_cast<const float2*>(sp.ml + 2 * at);
+        o[u] = *reinterpret_cast<const f32x4*>(sp.o + at * D + 4 * c);
         if (i >= ns) ml[u] = make_float2(-INFINITY, 0.f);
       }
 #pragma unroll
@@ -894,51 +900,79 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int decode_r
 
 // ---------------------------------------------------------------------------
 // The plan, from sizes alone (the lengths are on the device).
-AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv) {
-  (void)D;
+AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv,
+                        int64_t window) {
   const int64_t G = Hq / Hkv;
   AttnPlan p;
+  p.D = D;
   max_q = std::min(max_q, T);
   max_kv = std::min<int64_t>(max_kv, 1 << 30);
   const int64_t max_rows = max_q * G;
-  p.prefill = max_rows > 64;
-  // with the prefill kernel the decode kernel takes the short sequences of a
-  // mixed batch only
-  p.decode_tiles = std::min<int64_t>(max_rows, 64) <= 16 && !p.prefill ? 1 : 2;
-  if (!p.prefill) p.row_limit = 0x7FFFFFFF;
-  else if (B * max_q == T) p.row_limit = p.decode_tiles = 0;  // no short ones, by what we are told
-  else p.row_limit = 64;
-  // Chunks: long enough that a workgroup's start (about 4 us of dependent reads)
-  // is small beside its stream, short enough that ragged lengths spread over the
-  // chip and that 512 workgroups, two a CU, exist.  64 sequences of 500 .. 16384
-  // tokens, 8 heads: 203 us with chunks of 2048, 209 with 4096, 240 with 8192; 2 of
-  // 131072 with 32 rows: 99 us with 4096, 114 with 2048, 132 with 1024.
-  const int64_t tile = p.prefill ? kPrefillRows : 16 * p.decode_tiles;
-  const int64_t tiles = std::max<int64_t>(1, std::max<int64_t>(T * G / tile, std::min(B, T))) * Hkv;
-  const int64_t unit = p.prefill ? 512 : 256;
-  const int64_t most = p.prefill ? max_kv : p.decode_tiles == 1 ? 2048 : 4096;
-  const int64_t ns = std::max<int64_t>(1, 512 / tiles);
-  int64_t chunk = std::min((max_kv + ns - 1) / ns, most);
-  chunk = std::max<int64_t>(unit, (chunk + unit - 1) / unit * unit);
-  p.chunk = (int)chunk;
-  p.nsplit = (int)std::max<int64_t>(1, (max_kv + chunk - 1) / chunk);
+  // tokens that a tile of rows sees at most
+  const auto reach = [&](int64_t rows) {
+    return window ? std::min(max_kv, window + 64 + rows / G) : max_kv;
+  };
+  // tokens a split: `most`, or less to make 512 workgroups (two a CU), but not
+  // below `least`
+  const auto split = [&](int64_t tiles, int64_t kv, int64_t least, int64_t most) {
+    const int64_t ns = std::max<int64_t>(1, 512 / std::max<int64_t>(tiles, 1));
+    int64_t chunk = std::min((kv + ns - 1) / ns, most);
+    chunk = std::max(least, (chunk + 255) / 256 * 256);
+    AttnSplit s{};
+    s.chunk = (int)chunk;
+    s.n = (int)std::max<int64_t>(1, (kv + chunk - 1) / chunk);
+    s.rows = T * Hq;
+    return s;
+  };
+  p.few_split = p.many_split = AttnSplit{1, 256, T * Hq, nullptr, nullptr};
+  p.few_by_seq = false;
+  p.many = max_rows > kFewRows;
+  p.few_tiles = 0;
+  p.row_limit = 0;
+  if (p.many) {
+    const int64_t tiles = std::max(T * G / kPrefillRows, std::min(B, T)) * Hkv;
+    p.many_split = split(tiles, reach(kPrefillRows), 512, 1 << 30);
+  }
+  // The short sequences of a mixed batch: the kernel for many rows computes them
+  // in passing where they see few tokens; with more, one workgroup of it would be
+  // busy with each long after the others (and sequences that are all long, by what
+  // we are told, leave nothing to do).
+  const bool short_ones = !p.many || (B * max_q != T && reach(kFewRows) > 2048);
+  if (short_ones) {
+    // Chunks: long enough that a workgroup's start (about 4 us of dependent reads)
+    // is small beside its stream, short enough that ragged lengths spread over the
+    // chip.  64 sequences of 500 .. 16384 tokens, 8 heads: 203 us with 2048, 209
+    // with 4096, 240 with 8192; 2 of 131072 with 32 rows: 99 us with 4096, 114 with
+    // 2048, 132 with 1024.  One workgroup streams 1024 tokens in about the time that
+    // the join takes.
+    p.few_tiles = std::min<int64_t>(max_rows, kFewRows) <= 16 ? 1 : 2;
+    p.row_limit = p.many ? kFewRows : 0x7FFFFFFF;
+    const int64_t few_T = p.many ? std::min(B, T) : T;
+    const int64_t tiles = std::max(few_T * G / (16 * p.few_tiles), std::min(B, T)) * Hkv;
+    p.few_split = split(tiles, reach(16 * p.few_tiles), 1024, p.few_tiles == 1 ? 2048 : 4096);
+    if (p.many && B * kFewRows * Hkv < T * Hq) {
+      p.few_by_seq = true;
+      p.few_split.rows = B * kFewRows * Hkv;
+    }
+  }
   return p;
 }
 
 template <bool F16, int D>
-static void attn_launch(AttnArgs a, const AttnPlan& p, hipStream_t s) {
+static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int64_t R = (int64_t)a.kb.T * a.G;
-  if (p.prefill)
-    attn_prefill_kernel<F16, D><<<grid_of(prefill_slots(a) * a.c.heads * a.nsplit), 256, 0, s>>>(a);
-  if (p.decode_tiles == 1)
+  if (p.many)
+    attn_prefill_kernel<F16, D><<<grid_of(prefill_slots(a) * a.c.heads * a.many.n), 256, 0, s>>>(a);
+  if (p.few_tiles == 1)
     attn_decode_kernel<F16, D, 1><<<grid_of((R / 16 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
-  else if (p.decode_tiles == 2)
+  else if (p.few_tiles == 2)
     attn_decode_kernel<F16, D, 2><<<grid_of((R / 32 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
   const int64_t out_rows = (int64_t)a.kb.T * a.Hq;
-  if (p.nsplit > 8)
-    attn_join_kernel<F16, D, 4><<<grid_of(out_rows), 256, 0, s>>>(a, 16 * p.decode_tiles);
-  else if (p.nsplit > 1)
-    attn_join_kernel<F16, D, 1><<<grid_of((out_rows + 3) / 4), 256, 0, s>>>(a, 16 * p.decode_tiles);
+  const int n = std::max(p.few_split.n, p.many_split.n), few_rows = 16 * std::max(p.few_tiles, 1);
+  if (n > 8)
+    attn_join_kernel<F16, D, 4><<<grid_of(out_rows), 256, 0, s>>>(a, few_rows);
+  else if (n > 1)
+    attn_join_kernel<F16, D, 1><<<grid_of((out_rows + 3) / 4), 256, 0, s>>>(a, few_rows);
 }
 
 hipError_t launch_attention(const AttnArgs& a, bool f16, const AttnPlan& p, hipStream_t s) {

@@ -165,6 +165,15 @@ hipError_t launch_kv_write(const void* k, const void* v, bool f16, int64_t ld_k,
 hipError_t launch_kv_read(const KvBatch& kb, const KvCache& c, void* k, void* v, bool f16,
                           int64_t ld_k, int64_t ld_v, hipStream_t s);
 
+// How one of the two attention kernels splits the cached tokens of its rows:
+// `n` splits at most, of `chunk` tokens.  Unjoined results: o [n][rows][D] and ml
+// [n][rows][2] (maximum, sum).
+struct AttnSplit {
+  int n, chunk;
+  int64_t rows;
+  float *o, *ml;
+};
+
 struct AttnArgs {
   const uint16_t* q;
   int64_t ld_q;
@@ -177,20 +186,29 @@ struct AttnArgs {
   float scale_log2;  // |softmax scale| * log2(e), above 0
   int negate;        // the scale is negative: the queries are negated instead
   int causal, window;
-  // split over the cached tokens: a row tile's split s covers `chunk` tokens;
-  // part_o [split][T][Hq][D], part_ml [split][T][Hq] hold unjoined results
-  int nsplit, chunk;
-  float* part_o;
-  float* part_ml;
-  int row_limit;  // sequences of at most this many rows (tokens x G) are the decode kernel's
+  AttnSplit few, many;  // of the kernel for few rows, and of the one for many
+  int few_by_seq;       // unjoined rows of `few` are [sequence][kFewRows][head], else [T][Hq]
+  int row_limit;        // sequences of at most this many rows (tokens x G) are few's
 };
+constexpr int kFewRows = 64;  // row_limit where both kernels run
+
 struct AttnPlan {
-  int decode_tiles;  // 16-row tiles of a decode workgroup, 0: the decode kernel is not launched
-  bool prefill;      // the prefill kernel is launched
+  int few_tiles;  // 16-row tiles of a workgroup of few rows, 0: not launched
+  bool many;      // the kernel for many rows is launched
   int row_limit;
-  int nsplit, chunk;
+  bool few_by_seq;
+  AttnSplit few_split, many_split;  // (no addresses)
+  size_t bytes() const { return offset_many() + part_bytes(many_split); }
+  size_t offset_many() const { return part_bytes(few_split); }
+  int D;
+
+ private:
+  size_t part_bytes(const AttnSplit& s) const {
+    return s.n > 1 ? (size_t)s.n * (size_t)s.rows * (size_t)(D + 2) * sizeof(float) : 0;
+  }
 };
-AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv);
+AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv,
+                        int64_t window);
 hipError_t launch_attention(const AttnArgs& a, bool f16, const AttnPlan& p, hipStream_t s);
 
 }  // namespace fp8sm

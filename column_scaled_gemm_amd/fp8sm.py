@@ -60,7 +60,8 @@ SIGNATURES = {
                                      _p, _p, _p, _i64, _i32, _i32, _i32, _i64, _i64,
                                      ctypes.c_float, _u32, _i32, _p, _i64, _p, _p,
                                      ctypes.c_size_t, _p]),
-    "fp8sm_attention_cache_workspace": (ctypes.c_size_t, [_i64, _i64, _i32, _i32, _i32, _i64, _i64]),
+    "fp8sm_attention_cache_workspace": (ctypes.c_size_t, [_i64, _i64, _i32, _i32, _i32, _i64, _i64,
+                                                          _i32]),
     "fp8sm_scale_bytes": (ctypes.c_size_t, [_int, _int, _i64, _i64, _i32]),
     "fp8sm_status_str": (ctypes.c_char_p, [_int]),
     "fp8sm_force_variant": (_int, [_int]),
@@ -789,10 +790,10 @@ def kv_cache_read(cache, cu, lens, table, total, dtype=torch.bfloat16, k=None, v
     return k, v
 
 
-def attention_cache_workspace(T, nseq, q_heads, kv_heads, head_dim, max_q, max_kv):
+def attention_cache_workspace(T, nseq, q_heads, kv_heads, head_dim, max_q, max_kv, window=0):
     """Bytes of workspace of an attention_cache call of these sizes."""
     return _load().fp8sm_attention_cache_workspace(T, nseq, q_heads, kv_heads, head_dim, max_q,
-                                                   max_kv)
+                                                   max_kv, window)
 
 
 def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, causal=True,
@@ -823,7 +824,7 @@ def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, c
     if max_kv is None:
         max_kv = n * block
     L = _load()
-    need = L.fp8sm_attention_cache_workspace(T, B, Hq, H, D, max_q, max_kv)
+    need = L.fp8sm_attention_cache_workspace(T, B, Hq, H, D, max_q, max_kv, window)
     if workspace is not None:
         _holds_bytes(workspace, need, "workspace", torch.uint8)
     elif need:

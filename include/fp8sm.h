@@ -442,7 +442,7 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
 /* Bytes of workspace for an fp8sm_attention_cache call of these sizes (0 on
  * invalid input: the call itself reports it). */
 size_t fp8sm_attention_cache_workspace(int64_t T, int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
-                                       int64_t max_q, int64_t max_kv);
+                                       int64_t max_q, int64_t max_kv, int32_t window);
 
 /* Bytes needed for the scales of fp8sm_quant_group (0 on invalid input). */
 size_t fp8sm_scale_bytes(fp8sm_scale_fmt fmt, fp8sm_scale_layout lay, int64_t M, int64_t K_out,
