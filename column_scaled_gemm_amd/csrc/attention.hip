@@ -64,6 +64,23 @@ __device__ __forceinline__ uint32_t token_bytes(int t, int lo, int hi) {
   return m;
 }
 
+// The NaN codes (0x7F, 0xFF) of four, as the top bits of their bytes.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t v) {
+  return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+// Their bytes, all bits.
+__device__ __forceinline__ uint32_t byte_mask(uint32_t top) { return (top >> 7) * 0xFFu; }
+// 1.0 for each of eight NaN codes, 0 for the others.
+__device__ __forceinline__ f16x8 nan_ones(uint32_t n0, uint32_t n1) {
+  f16x8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = (n0 >> (8 * i)) & 0x80u ? (_Float16)1.f : (_Float16)0.f;
+    r[4 + i] = (n1 >> (8 * i)) & 0x80u ? (_Float16)1.f : (_Float16)0.f;
+  }
+  return r;
+}
+
 // The tokens that the rows [r0, r1) of a sequence see, [lo, hi), and the first
 // token of their split 0 (a multiple of 64).
 struct Span {
@@ -116,15 +133,15 @@ __device__ __forceinline__ float quarter_max(float v) {
 // 4 g .. 4 g + 3.  Of a step's 64 tokens, key tile t (0..3) takes as its row m
 // token 16 (m / 4) + 4 t + m % 4, so that lane quarter g ends up with the
 // scores of the consecutive tokens 16 g .. 16 g + 15.
-constexpr int kDecodeRuns = 256;  // runs of 16 tokens a gather brings
+constexpr int kFewRuns = 256;  // runs of 16 tokens a gather brings
 
-__host__ __device__ __forceinline__ int decode_stride(const AttnArgs& a) { return a.c.heads * a.few.n | 1; }
+__host__ __device__ __forceinline__ int few_stride(const AttnArgs& a) { return a.c.heads * a.few.n | 1; }
 
 template <bool F16, int D, int QT>
-__global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
   constexpr int NI = D / 64, DT = D / 16;
-  __shared__ int64_t mat[kDecodeRuns];  // a run's place in both code arrays, -1: no block
-  __shared__ float mks[kDecodeRuns], mvs[kDecodeRuns];
+  __shared__ int64_t mat[kFewRuns];  // a run's place in both code arrays, -1: no block
+  __shared__ float mks[kFewRuns], mvs[kFewRuns];
   using op8 = std::conditional_t<F16, f16x8, bf16x8>;
   const int lane = threadIdx.x & 63, x = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -133,7 +150,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
   // XCDs in turn.  An odd number of them a row tile (one idle) keeps any stride
   // of idle tiles or of short sequences from falling on the same XCDs (with an
   // even one, 154 us where 106 were due).
-  const int per = decode_stride(a), id = (int)(workgroup_id() % per);
+  const int per = few_stride(a), id = (int)(workgroup_id() % per);
   const int64_t slot = workgroup_id() / per;
   if (id >= a.c.heads * a.few.n) return;
   const int hk = id % a.c.heads, split = id / a.c.heads;
@@ -207,7 +224,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
   // of 8 heads).
   const int last_run = max((t_end - 1) >> 4, 0);
   uint4 kc[4][NI], vc[DT];
-  for (int seg = t_begin; seg < t_end; seg += 16 * kDecodeRuns) {
+  for (int seg = t_begin; seg < t_end; seg += 16 * kFewRuns) {
     if (seg > t_begin) __syncthreads();  // nobody reads the last segment's any more
     {
       const int run = (seg >> 4) + threadIdx.x;
@@ -227,7 +244,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
       mvs[threadIdx.x] = vs;
     }
     __syncthreads();
-    const int seg_end = min(t_end, seg + 16 * kDecodeRuns);
+    const int seg_end = min(t_end, seg + 16 * kFewRuns);
     auto fetch_k = [&](int t0) {
       const int64_t at = max(mat[((t0 - seg) >> 4) + (x >> 2)], (int64_t)0);
       const uint8_t* kb = a.c.k + at + (x & 3) * D + 16 * g;
@@ -343,6 +360,28 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
           vc[d].y &= keep[1];
           vc[d].z &= keep[2];
           vc[d].w &= keep[3];
+          // a NaN code that some rows see and others do not: see attn_many_kernel
+          const uint32_t n0 = nan_codes(vc[d].x), n1 = nan_codes(vc[d].y), n2 = nan_codes(vc[d].z),
+                         n3 = nan_codes(vc[d].w);
+          if (!__any((n0 | n1 | n2 | n3) != 0)) continue;
+#pragma unroll
+          for (int i = 0; i < QT; ++i) {
+            f16x8 vis[2];
+            const int from = bad ? 0x7FFFFFFF : see_lo[i];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              vis[k >> 3][k & 7] = t + k < from || t + k >= see_hi[i] ? (_Float16)0.f : (_Float16)1.f;
+            f32x4 z = {0.f, 0.f, 0.f, 0.f};
+            z = __builtin_amdgcn_mfma_f32_16x16x32_f16(nan_ones(n0, n1), vis[0], z, 0, 0, 0);
+            z = __builtin_amdgcn_mfma_f32_16x16x32_f16(nan_ones(n2, n3), vis[1], z, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (z[k] > 0.f) o[i][d][k] = __builtin_nanf("");
+          }
+          vc[d].x &= ~byte_mask(n0);
+          vc[d].y &= ~byte_mask(n1);
+          vc[d].z &= ~byte_mask(n2);
+          vc[d].w &= ~byte_mask(n3);
         }
       }
 #pragma unroll
@@ -438,7 +477,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(AttnArgs a) {
 // bit, 2^-9, still is a fp16 value).  Wider ranges take V in bf16 and P as the
 // sum of two bf16 values (WIDE).  Sums are fp32.
 //
-constexpr int kPrefillRows = 128, kPrefillStep = 64, kPrefillSlots = 3;
+constexpr int kManyRows = 128, kManyStep = 64, kManySlots = 3;
 constexpr int kMetaSteps = 32;  // steps whose runs' blocks and scales one gather brings
 
 // 16-byte global -> LDS copy: reads base + off, lane i writes lds + 16 i.
@@ -459,18 +498,18 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-__host__ __device__ __forceinline__ int64_t prefill_slots(const AttnArgs& a) {
-  return (int64_t)a.kb.T * a.G / kPrefillRows + a.kb.B;
+__host__ __device__ __forceinline__ int64_t many_slots(const AttnArgs& a) {
+  return (int64_t)a.kb.T * a.G / kManyRows + a.kb.B;
 }
 
 template <bool F16, int D>
-__global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   constexpr int DT = D / 32, NP = D / 32;  // channel tiles; 16-byte pieces of a lane's key row
   constexpr int RUN = 16 * D;              // bytes of a run's keys or values
   constexpr int TILE = 4 * RUN;
   constexpr int CPW = 2 * RUN / 1024;      // copies of a wavefront a step
   using op8 = std::conditional_t<F16, f16x8, bf16x8>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[kPrefillSlots][2][TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kManySlots][2][TILE];
   __shared__ __attribute__((aligned(16))) int mpage[2][4 * kMetaSteps];  // block, -1: none
   __shared__ float mks[2][4 * kMetaSteps], mvs[2][4 * kMetaSteps];
   __shared__ int sref[12];
@@ -482,7 +521,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   // with more work, each takes a contiguous part of the list, so that the tiles
   // that read the same keys share an L2 (8320 tokens, 56 heads: 1237 us in
   // list order, 1147 so; tiles in ascending order 1197).
-  const int64_t slots = prefill_slots(a), n = slots * a.c.heads * a.many.n, id = workgroup_id();
+  const int64_t slots = many_slots(a), n = slots * a.c.heads * a.many.n, id = workgroup_id();
   if (id >= n) return;
   const int pairs = a.c.heads * a.many.n;
   const int64_t part = n >> 3, rest = n & 7;
@@ -494,17 +533,17 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   const int b = find_seq(a.kb, slot, a.G, 7, 1, &f0);
   const Seq s = load_seq(a.kb, b, bs);
   const int rows = s.n * a.G;
-  const int64_t r64 = (slot - f0) * kPrefillRows;
+  const int64_t r64 = (slot - f0) * kManyRows;
   if (r64 >= rows || rows <= a.row_limit) return;
   const int r0 = (int)r64;
-  const Span sp = row_span(a, a.many, s, r0, min(r0 + kPrefillRows, rows));
+  const Span sp = row_span(a, a.many, s, r0, min(r0 + kManyRows, rows));
   const int ns = sp.splits;
   if (split >= max(ns, 1)) return;
   const int t_begin = sp.start + split * sp.chunk;
   const int t_end = min(sp.hi, t_begin + sp.chunk);
   const int32_t* table = a.kb.table + (int64_t)b * a.kb.ld_table;
   const int in_mask = (1 << (bs - 4)) - 1;
-  const int steps = t_end > t_begin ? (t_end - t_begin + kPrefillStep - 1) / kPrefillStep : 0;
+  const int steps = t_end > t_begin ? (t_end - t_begin + kManyStep - 1) / kManyStep : 0;
 
   // the largest and smallest value exponents of the blocks in reach, and
   // whether one is missing
@@ -613,7 +652,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
     const int run = __builtin_amdgcn_readfirstlane(first_run + 4 * i + w);
     const int page = max(__builtin_amdgcn_readfirstlane(mpage[(i / kMetaSteps) & 1][4 * (i % kMetaSteps) + w]), 0);
     const int64_t at = ((((int64_t)page * a.c.heads + hk) << bs) + ((run & in_mask) << 4)) * D;
-    const uint32_t dst = lds0 + (uint32_t)(i % kPrefillSlots) * (2 * TILE) + w * RUN;
+    const uint32_t dst = lds0 + (uint32_t)(i % kManySlots) * (2 * TILE) + w * RUN;
     copy16<0>(a.c.k + at, koff, dst);
     if constexpr (D == 128) copy16<0>(a.c.k + at + 1024, koff, dst + 1024);
     copy16<0>(a.c.v + at, lane * 16, dst + TILE);
@@ -627,9 +666,9 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
   // One step.  PARTIAL: some row does not see some of its tokens.
   auto compute = [&](int i, auto wide_tag, auto partial_tag) {
     constexpr bool WIDE = decltype(wide_tag)::value, PARTIAL = decltype(partial_tag)::value;
-    const int t0 = t_begin + i * kPrefillStep;
-    const uint8_t* lk = ring[i % kPrefillSlots][0];
-    const uint8_t* lv = ring[i % kPrefillSlots][1];
+    const int t0 = t_begin + i * kManyStep;
+    const uint8_t* lk = ring[i % kManySlots][0];
+    const uint8_t* lv = ring[i % kManySlots][1];
     const int mb = (i / kMetaSteps) & 1, mi = 4 * (i % kMetaSteps);
     f32x16 sc[2];
 #pragma unroll
@@ -698,6 +737,27 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
         sum += sc[grp][k];
       }
       l += sum;
+      // A NaN code that some rows see and others do not: a product with the others'
+      // p = 0 would give them NaN too.  Such codes become 0, and the rows that see one
+      // are found by a product of their own.
+      auto clear_nan = [&](uint4& c, f32x16& od) {
+        const uint32_t n0 = nan_codes(c.x), n1 = nan_codes(c.y), n2 = nan_codes(c.z), n3 = nan_codes(c.w);
+        if (!__any((n0 | n1 | n2 | n3) != 0)) return;
+        const int t = t0 + 32 * grp + 16 * h;
+        const int lo = mpage[mb][mi + 2 * grp + h] < 0 ? 0x7FFFFFFF : see_lo;
+        f16x8 vis[2];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) vis[k >> 3][k & 7] = t + k < lo || t + k >= see_hi ? (_Float16)0.f : (_Float16)1.f;
+        f32x16 z;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) z[k] = 0.f;
+        z = __builtin_amdgcn_mfma_f32_32x32x16_f16(nan_ones(n0, n1), vis[0], z, 0, 0, 0);
+        z = __builtin_amdgcn_mfma_f32_32x32x16_f16(nan_ones(n2, n3), vis[1], z, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (z[k] > 0.f) od[k] = __builtin_nanf("");
+        c.x &= ~byte_mask(n0), c.y &= ~byte_mask(n1), c.z &= ~byte_mask(n2), c.w &= ~byte_mask(n3);
+      };
       if constexpr (WIDE) {
         bf16x8 ph[2], pl[2];
 #pragma unroll
@@ -709,7 +769,10 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           uint4 c = *reinterpret_cast<const uint4*>(vrow + 512 * d);
-          if constexpr (PARTIAL) c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
+          if constexpr (PARTIAL) {
+            c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
+            clear_nan(c, o[d]);
+          }
           const bf16x8 v0 = widen_bf16(c.x, c.y, vs), v1 = widen_bf16(c.z, c.w, vs);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, ph[0], o[d], 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, pl[0], o[d], 0, 0, 0);
@@ -723,7 +786,10 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           uint4 c = *reinterpret_cast<const uint4*>(vrow + 512 * d);
-          if constexpr (PARTIAL) c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
+          if constexpr (PARTIAL) {
+            c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
+            clear_nan(c, o[d]);
+          }
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, vs), p[0], o[d], 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, vs), p[1], o[d], 0, 0, 0);
         }
@@ -748,8 +814,8 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
     auto masked = [&](int from, int to) {
       for (int i = from; i < to; ++i) {
         advance(i);
-        const int t0 = t_begin + i * kPrefillStep;
-        if (t0 < w_hi && t0 + kPrefillStep > w_lo) compute(i, wide_tag, std::true_type{});
+        const int t0 = t_begin + i * kManyStep;
+        if (t0 < w_hi && t0 + kManyStep > w_lo) compute(i, wide_tag, std::true_type{});
       }
     };
     gather(0);
@@ -761,8 +827,8 @@ __global__ __launch_bounds__(256, 2) void attn_prefill_kernel(AttnArgs a) {
     } else {
       int from = steps, to = steps;  // with missing blocks every step is masked
       if (!missing) {
-        from = min(max((all_lo - t_begin + kPrefillStep - 1) / kPrefillStep, 0), steps);
-        to = min(max((all_hi - t_begin) / kPrefillStep, from), steps);
+        from = min(max((all_lo - t_begin + kManyStep - 1) / kManyStep, 0), steps);
+        to = min(max((all_hi - t_begin) / kManyStep, from), steps);
       }
       masked(0, from);
       for (int i = from; i < to; ++i) {
@@ -834,7 +900,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int few_rows
   const int rows = s.n * a.G;
   const bool few = rows <= a.row_limit;
   const AttnSplit& sp = few ? a.few : a.many;
-  const int tile = few ? few_rows : kPrefillRows;
+  const int tile = few ? few_rows : kManyRows;
   const int r = (t - s.c0) * a.G + head % a.G, r0 = r / tile * tile;
   int ns = 0;
   if (there && t >= s.c0 && t < s.c0 + s.n)  // some sequence's row
@@ -930,8 +996,8 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
   p.few_tiles = 0;
   p.row_limit = 0;
   if (p.many) {
-    const int64_t tiles = std::max(T * G / kPrefillRows, std::min(B, T)) * Hkv;
-    p.many_split = split(tiles, reach(kPrefillRows), 512, 1 << 30);
+    const int64_t tiles = std::max(T * G / kManyRows, std::min(B, T)) * Hkv;
+    p.many_split = split(tiles, reach(kManyRows), 512, 1 << 30);
   }
   // The short sequences of a mixed batch: the kernel for many rows computes them
   // in passing where they see few tokens; with more, one workgroup of it would be
@@ -962,11 +1028,11 @@ template <bool F16, int D>
 static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int64_t R = (int64_t)a.kb.T * a.G;
   if (p.many)
-    attn_prefill_kernel<F16, D><<<grid_of(prefill_slots(a) * a.c.heads * a.many.n), 256, 0, s>>>(a);
+    attn_many_kernel<F16, D><<<grid_of(many_slots(a) * a.c.heads * a.many.n), 256, 0, s>>>(a);
   if (p.few_tiles == 1)
-    attn_decode_kernel<F16, D, 1><<<grid_of((R / 16 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
+    attn_few_kernel<F16, D, 1><<<grid_of((R / 16 + a.kb.B) * few_stride(a)), 256, 0, s>>>(a);
   else if (p.few_tiles == 2)
-    attn_decode_kernel<F16, D, 2><<<grid_of((R / 32 + a.kb.B) * decode_stride(a)), 256, 0, s>>>(a);
+    attn_few_kernel<F16, D, 2><<<grid_of((R / 32 + a.kb.B) * few_stride(a)), 256, 0, s>>>(a);
   const int64_t out_rows = (int64_t)a.kb.T * a.Hq;
   const int n = std::max(p.few_split.n, p.many_split.n), few_rows = 16 * std::max(p.few_tiles, 1);
   if (n > 8)

@@ -49,7 +49,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-constexpr int kRopeU = 2;
+// 16-byte streaming store, as store_stream8.
+__device__ __forceinline__ void store_stream16(void* p, const uint4 v) {
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
+}
+
+constexpr int kRopeU = 4;  // (8320 rows of 112 heads: 1: 119 us, 2: 108, 4: 100)
 
 template <bool F16, int D, bool NORM, bool INTER>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
@@ -61,6 +66,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + t * a.ld_x;
   uint16_t* y = static_cast<uint16_t*>(a.y) + t * a.ld_y;
   const int h0 = (blockIdx.y * 4 + w) * (HPW * kRopeU) + sub;
+  if (h0 - sub >= heads) return;
 
   int64_t p = 0;
   if (a.rot) {
@@ -140,9 +146,9 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
       }
     }
     if (h < heads)
-      *reinterpret_cast<uint4*>(y + (int64_t)h * D + lh * 8) =
-          make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]),
-                     pack2<F16>(f[6], f[7]));
+      store_stream16(y + (int64_t)h * D + lh * 8,
+                     make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]),
+                                pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7])));
   }
 }
 
@@ -476,7 +482,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
         o[2 * k] = pack2<F16>(value(lo2[0]), value(lo2[1]));
         o[2 * k + 1] = pack2<F16>(value(hi2[0]), value(hi2[1]));
       }
-      *reinterpret_cast<uint4*>(dst + p * ld + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+      store_stream16(dst + p * ld + c * 8, make_uint4(o[0], o[1], o[2], o[3]));
     }
   } else {
     constexpr int TG = 128 / D, TPL = 16 / TG;

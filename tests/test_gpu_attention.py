@@ -254,3 +254,49 @@ def test_the_run_from_the_projection_to_the_output_projection():
         qa, sa = fp8sm.quant_group(out.flatten(1), -1)
         y = fp8sm.scaled_mm(qa, qo, sa.reshape(-1), so.reshape(-1), fp8sm.KIND_ROW, fp8sm.KIND_COL)
         assert y.shape == (sum(n), hid) and bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,lens,Hq,wide", [([5], [70], 2, False), ([9], [300], 3, False), ([150], [190], 1, False),
+                                            ([150], [190], 1, True)])
+@pytest.mark.parametrize("window", [0, 60])
+def test_nan_tokens_reach_only_the_rows_that_see_them(n, lens, Hq, wide, window, dtype, D):
+    """A NaN key makes every output of a row that sees it NaN, a NaN value its
+    channel; the other rows are as if it were not there."""
+    print(f"[case] nan {n} {lens} {Hq} {wide} {window} {dtype} {D}", flush=True)
+    r = rng(40 + D)
+    cu, L, table, blocks = batch(r, n, lens, 16)
+    ref = random_cache(r, blocks, 1, 16, D)
+    if wide:
+        ref.exp[1][:] = r.integers(100, 125, ref.exp[1].shape)
+    T, ln = n[0], lens[0]
+    q = torch.from_numpy(r.standard_normal((T, Hq, D)).astype(np.float32)).to(DT[dtype]).cuda()
+    clean = okv.Cache(ref.codes[0], ref.codes[1], *ref.exp)
+    # a NaN value in the last token but two of channel 3, one further back, a NaN key
+    for which, pos, ch in ((1, ln - 3, 3), (1, ln - T + 1, 5), (1, 2, 7), (0, ln - 2, 1)):
+        page, slot = table[0, pos // 16], pos % 16
+        c = ref.get(which, page, slot, 0).copy()
+        c[ch] = 0xFF
+        ref.put(which, page, slot, 0, c)
+    d = to_dev(cu, L, table)
+    out, lse = fp8sm.attention_cache(q, dev_cache(ref), *d, T, window=window, return_lse=True)
+    o, s, spread, qk = okv.attention(q.double().cpu().numpy(), clean, cu, L, table, D ** -0.5, True, window)
+    to, tl = attention_bounds(o, s, spread, qk, D ** -0.5, D, ln, dtype)
+    pos = np.arange(ln - T, ln)[:, None]
+
+    def sees(p):
+        return ((p <= pos) & (p > pos - window) if window else p <= pos)[:, 0]
+
+    want = np.zeros((T, Hq, D), dtype=bool)
+    want[sees(ln - 3), :, 3] = True
+    want[sees(ln - T + 1), :, 5] = True
+    want[sees(2), :, 7] = True
+    want[sees(ln - 2)] = True
+    g, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isnan(g), want)
+    assert np.array_equal(np.isnan(gl), np.broadcast_to(sees(ln - 2)[:, None], gl.shape))
+    # the clean cache differs in tokens that these rows see with other codes: compare rows that see none
+    none = ~(sees(ln - 3) | sees(ln - T + 1) | sees(2) | sees(ln - 2))
+    if none.any():
+        assert np.all(np.abs(g - o)[none] <= to[none]) and np.all(np.abs(gl - s)[none] <= tl[none])
