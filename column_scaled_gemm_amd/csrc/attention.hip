@@ -154,11 +154,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
   const int64_t slot = workgroup_id() / per;
   if (id >= a.c.heads * a.few.n) return;
   const int hk = id % a.c.heads, split = id / a.c.heads;
-  int64_t f0;
-  const int b = find_seq(a.kb, slot, a.G, QT == 2 ? 5 : 4, 1, &f0);
-  const Seq s = load_seq(a.kb, b, bs);
+  const Seq s = find_seq(a.kb, bs, slot, a.G, QT == 2 ? 5 : 4, 1);
+  const int b = s.b;
   const int rows = s.n * a.G;
-  const int64_t r64 = (slot - f0) * (16 * QT);
+  const int64_t r64 = (slot - s.first) * (16 * QT);
   if (r64 >= rows || rows > a.row_limit) return;
   const int r0 = (int)r64;
   const Span sp = row_span(a, a.few, s, r0, min(r0 + 16 * QT, rows));
@@ -529,11 +528,10 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   const int64_t pair = at / slots, k = at - pair * slots;
   const int64_t slot = slots - 1 - k;
   const int hk = (int)(pair / a.many.n), split = (int)(pair - (int64_t)hk * a.many.n);
-  int64_t f0;
-  const int b = find_seq(a.kb, slot, a.G, 7, 1, &f0);
-  const Seq s = load_seq(a.kb, b, bs);
+  const Seq s = find_seq(a.kb, bs, slot, a.G, 7, 1);
+  const int b = s.b;
   const int rows = s.n * a.G;
-  const int64_t r64 = (slot - f0) * kManyRows;
+  const int64_t r64 = (slot - s.first) * kManyRows;
   if (r64 >= rows || rows <= a.row_limit) return;
   const int r0 = (int)r64;
   const Span sp = row_span(a, a.many, s, r0, min(r0 + kManyRows, rows));
@@ -894,9 +892,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int few_rows
   const int64_t id = workgroup_id() * (4 / WPR) + wave / WPR;
   const bool there = id < (int64_t)a.kb.T * a.Hq;
   const int t = there ? (int)(id / a.Hq) : 0, head = there ? (int)(id - (int64_t)t * a.Hq) : 0;
-  int64_t f0;
-  const int b = find_seq(a.kb, t, 1, 0, 0, &f0);
-  const Seq s = load_seq(a.kb, b, a.c.block_shift);
+  const Seq s = find_seq(a.kb, a.c.block_shift, t, 1, 0, 0);
+  const int b = s.b;
   const int rows = s.n * a.G;
   const bool few = rows <= a.row_limit;
   const AttnSplit& sp = few ? a.few : a.many;

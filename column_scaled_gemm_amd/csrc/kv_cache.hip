@@ -254,15 +254,13 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int bs = a.c.block_shift, block = W * TPW;
-  int64_t f0;
-  const int b = find_seq(a.kb, blockIdx.x, 1, bs, 2, &f0);
-  const Seq s = load_seq(a.kb, b, bs);
+  const Seq s = find_seq(a.kb, bs, blockIdx.x, 1, bs, 2);
   const int start = s.len - s.n;  // position of the first new token
   const int lo = max(start, 0);   // of the first one that has a place
-  const int j = (lo >> bs) + (int)(blockIdx.x - f0);
+  const int j = (lo >> bs) + (int)(blockIdx.x - s.first);
   const int p0 = j << bs;                                // first position of the block
   if (p0 >= s.len || lo >= s.len) return;                // the whole workgroup: no such block
-  const int page = a.kb.table[(int64_t)b * a.kb.ld_table + j];
+  const int page = a.kb.table[(int64_t)s.b * a.kb.ld_table + j];
   if (page < 0 || page >= a.c.num_blocks) return;        // no place
   const int H = a.c.heads;
   const int unit = blockIdx.y * (4 / W) + w / W;         // K heads, then V heads
@@ -437,9 +435,7 @@ template <bool F16, int D>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t f0;
-  const int b = find_seq(a.kb, blockIdx.x, 1, 4, 2, &f0);
-  const Seq s = load_seq(a.kb, b, a.c.block_shift);
+  const Seq s = find_seq(a.kb, a.c.block_shift, blockIdx.x, 1, 4, 2);
   const int start = s.len - s.n;
   const int H = a.c.heads;
   const int unit = blockIdx.y * 4 + w;
@@ -450,13 +446,13 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
   if (dst == nullptr) return;
   // runs of sixteen from the one that holds the first token (start < 0: those
   // tokens do not exist, their rows are zeros)
-  const int p0 = ((start >> 4) + (int)(blockIdx.x - f0)) << 4;
+  const int p0 = ((start >> 4) + (int)(blockIdx.x - s.first)) << 4;
   if (p0 >= s.len) return;
   const int lo = max(start - p0, 0), end = min(s.len - p0, 16);
   const int64_t ld = is_v ? a.ld_v : a.ld_k;
   dst += ((int64_t)s.c0 + p0 - start) * ld + h * D;  // row of the run's first token
   int page = -1;
-  if (p0 >= 0) page = a.kb.table[(int64_t)b * a.kb.ld_table + (p0 >> a.c.block_shift)];
+  if (p0 >= 0) page = a.kb.table[(int64_t)s.b * a.kb.ld_table + (p0 >> a.c.block_shift)];
   const bool ok = page >= 0 && page < a.c.num_blocks;
   const int64_t ph = (int64_t)(ok ? page : 0) * H + h;
   const float scale = ok ? exp_byte_value((is_v ? a.c.ve : a.c.ke)[ph]) : 0.f;

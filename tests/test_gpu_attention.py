@@ -19,7 +19,7 @@ def check(out, lse, q, ref, cu, L, table, scale, causal, window, dtype):
     assert np.array_equal(np.isneginf(gl[~np.isnan(s)]), np.isneginf(s[~np.isnan(s)]))
     err = np.abs(g - o)[mine] / to[mine]
     fin = np.isfinite(s)
-    err_l = (np.abs(gl - s)[fin] / tl[fin]) if fin.any() else np.zeros(1)
+    err_l = (np.abs(gl[fin] - s[fin]) / tl[fin]) if fin.any() else np.zeros(1)
     print(f"[bound] out {err.max() if err.size else 0:.3f} lse {err_l.max():.3f}", flush=True)
     assert np.all(err <= 1) and np.all(err_l <= 1)
     return mine
