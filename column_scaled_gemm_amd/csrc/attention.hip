@@ -126,7 +126,14 @@ __device__ __forceinline__ float quarter_max(float v) {
 // Few rows: 16 QT rows of one sequence and key head per workgroup, the cached
 // tokens split over the grid and over the four wavefronts, 64 tokens a step.
 // Bound by the stream of codes from memory; every code goes straight from
-// memory to the registers of the lane that multiplies it.
+// memory to the registers of the lane that multiplies it, widened there.  A chip
+// full of such workgroups streams 5.3 .. 5.9 TB/s (64 sequences of 500 .. 16384
+// tokens, 8 key heads of 128, 1.13 GB: 195 .. 202 us with the join; two of
+// 131072 tokens with 32 rows, 0.54 GB: 95 .. 101 us), above the 4.9 TB/s at
+// which a large copy reads and writes.
+// P is rounded to bf16 (half a step: 2^-8 of p) in bf16 calls; in fp16 calls it is
+// the sum of two bf16 values, so that V's widened codes stay exact in bf16 whatever
+// their blocks' scales.
 //
 // v_mfma_f32_16x16x32: lane l = 16 g + x holds row / column x and eight k
 // values of quarter g of both operands; of the result column x and rows
@@ -154,7 +161,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
   const int64_t slot = workgroup_id() / per;
   if (id >= a.c.heads * a.few.n) return;
   const int hk = id % a.c.heads, split = id / a.c.heads;
-  const Seq s = find_seq(a.kb, bs, slot, a.G, QT == 2 ? 5 : 4, 1);
+  // (where the long sequences are the other kernel's, a sequence has kFewRows rows at
+  // most: tiles are counted by sequences, not by rows)
+  const bool mixed = a.row_limit == kFewRows;
+  const Seq s = find_seq(a.kb, bs, slot, mixed ? 0 : a.G, QT == 2 ? 5 : 4, mixed ? kFewRows / (16 * QT) : 1);
   const int b = s.b;
   const int rows = s.n * a.G;
   const int64_t r64 = (slot - s.first) * (16 * QT);
@@ -218,9 +228,9 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
   // Keys of step i + 1 are loaded when those of step i are used up, its values
   // likewise, so one of them is always on its way.  Places and scales of the
   // runs of 16 tokens are gathered into LDS before (the plan's chunks need one
-  // gather): reading a block's number just before its codes made every step
-  // wait for two trips to memory (257 us instead of NEWLONG on 2 x 131072 tokens
-  // of 8 heads).
+  // gather): with the block's number read just before its codes, every step waited
+  // for two trips to memory (two sequences of 131072 tokens, 32 rows: 257 us, and
+  // 167 so, before the changes below and in the grid's order).
   const int last_run = max((t_end - 1) >> 4, 0);
   uint4 kc[4][NI], vc[DT];
   for (int seg = t_begin; seg < t_end; seg += 16 * kFewRuns) {
@@ -459,10 +469,20 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 // Many rows: 128 rows of one sequence and key head per workgroup, 32 a
-// wavefront, 64 tokens a step.  Wavefront w copies the step's run w of 16
-// tokens (keys and values, 2 KB each at D = 128) straight into an LDS ring of
-// three steps; a run lies in one block, so its address is wavefront-uniform.
-// Block numbers and scales are gathered 128 runs at a time into LDS.
+// wavefront, 64 tokens a step.  Wavefront w copies the step's run w of 16 tokens
+// (keys and values, 2 KB each at D = 128) straight into an LDS ring of three
+// steps; a run lies in one block, so its address is wavefront-uniform.  Block
+// numbers and scales are gathered 128 runs at a time into LDS.
+// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 1010 .. 1075 us, 0.92 .. 0.98
+// PFLOP/s, where a bf16 library product of 16384^3 reaches 1.36.  Bound by vector
+// arithmetic (63% busy: widening 128 of a step's 300 instructions, the rest
+// softmax), the matrix instructions beside it (44%) and the clock, which real data
+// lowers by a fifth (920 us with constant operands).  Slower, measured: widening
+// once per workgroup through LDS (1093 against 1033 us); eight wavefronts in
+// alternating phases held apart by barriers (1273); the next step's scores
+// beside this step's exponentials (no change); 64 rows a wavefront (registers
+// spill, 2119); 32 tokens at a time (1180 .. 1193); reads sent off as a block before
+// each product (1138 against 1077).
 //
 // v_mfma_f32_32x32x16: lane l = 32 h + x holds row / column x and eight k
 // values of half h of both operands; of the result column x and rows
@@ -983,7 +1003,9 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
     chunk = std::max(least, (chunk + 255) / 256 * 256);
     AttnSplit s{};
     s.chunk = (int)chunk;
-    s.n = (int)std::max<int64_t>(1, (kv + chunk - 1) / chunk);
+    // (the grid stays within bounds whatever the hints say: the chunks grow)
+    const int64_t cap = std::max<int64_t>(1, ((int64_t)1 << 22) / std::max<int64_t>(tiles, 1));
+    s.n = (int)std::min(std::max<int64_t>(1, (kv + chunk - 1) / chunk), cap);
     s.rows = T * Hq;
     return s;
   };
@@ -1026,10 +1048,13 @@ static void attn_launch(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int64_t R = (int64_t)a.kb.T * a.G;
   if (p.many)
     attn_many_kernel<F16, D><<<grid_of(many_slots(a) * a.c.heads * a.many.n), 256, 0, s>>>(a);
+  const auto few_slots = [&](int rows) {
+    return p.many ? (int64_t)a.kb.B * (kFewRows / rows) : R / rows + a.kb.B;
+  };
   if (p.few_tiles == 1)
-    attn_few_kernel<F16, D, 1><<<grid_of((R / 16 + a.kb.B) * few_stride(a)), 256, 0, s>>>(a);
+    attn_few_kernel<F16, D, 1><<<grid_of(few_slots(16) * few_stride(a)), 256, 0, s>>>(a);
   else if (p.few_tiles == 2)
-    attn_few_kernel<F16, D, 2><<<grid_of((R / 32 + a.kb.B) * few_stride(a)), 256, 0, s>>>(a);
+    attn_few_kernel<F16, D, 2><<<grid_of(few_slots(32) * few_stride(a)), 256, 0, s>>>(a);
   const int64_t out_rows = (int64_t)a.kb.T * a.Hq;
   const int n = std::max(p.few_split.n, p.many_split.n), few_rows = 16 * std::max(p.few_tiles, 1);
   if (n > 8)

@@ -300,3 +300,48 @@ def test_nan_tokens_reach_only_the_rows_that_see_them(n, lens, Hq, wide, window,
     none = ~(sees(ln - 3) | sees(ln - T + 1) | sees(2) | sees(ln - 2))
     if none.any():
         assert np.all(np.abs(g - o)[none] <= to[none]) and np.all(np.abs(gl - s)[none] <= tl[none])
+
+
+@pytest.mark.parametrize("n", [[1, 2], [70, 1]])
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_zero_and_negative_scale(n, scale):
+    print(f"[case] scale {scale} {n}", flush=True)
+    r = rng(50)
+    cu, L, table, blocks = batch(r, n, [130, 70], 16)
+    ref = random_cache(r, blocks, 2, 16, 64)
+    q = torch.from_numpy(r.standard_normal((sum(n), 4, 64)).astype(np.float32)).to(torch.bfloat16).cuda()
+    out, lse = fp8sm.attention_cache(q, dev_cache(ref), *to_dev(cu, L, table), max(n), scale=scale, return_lse=True)
+    o, s, spread, qk = okv.attention(q.double().cpu().numpy(), ref, cu, L, table, scale)
+    to, tl = attention_bounds(o, s, spread, qk, abs(scale), 64, 130, "bf16")
+    assert np.all(np.abs(out.double().cpu().numpy() - o) <= to)
+    assert np.all(np.abs(lse.double().cpu().numpy() - s) <= tl)
+
+
+@pytest.mark.parametrize("n", [[3], [80]])
+@pytest.mark.parametrize("ke,ve", [(85, 85), (100, 200), (85, 240)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_extreme_scales(n, ke, ve, dtype):
+    """Tiny keys and values, and values beyond fp16's range (bf16 results)."""
+    def damage(cu, L, table, ref):
+        ref.exp[0][:] = ke
+        ref.exp[1][:] = ve
+    if dtype == "fp16" and ve > 130:
+        return
+    run(n, [200], 2, 1, 64, 32, dtype, damage=damage)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_short_sequences_with_long_caches_in_a_mixed_batch(dtype, D):
+    """Both kernels run, each with splits of its own."""
+    run([90, 1, 0, 2, 30, 1], [2300, 5000, 70, 3100, 2100, 40], 4, 2, D, 64, dtype, max_kv=5000)
+
+
+def test_sequences_that_share_blocks():
+    r = rng(51)
+    cu, L, table, blocks = batch(r, [1, 70, 1], [100, 100, 33], 16)
+    table[1, :2], table[2, :2] = table[0, :2], table[0, :2]
+    ref = random_cache(r, blocks, 1, 16, 64)
+    q = torch.from_numpy(r.standard_normal((72, 3, 64)).astype(np.float32)).to(torch.float16).cuda()
+    out, lse = fp8sm.attention_cache(q, dev_cache(ref), *to_dev(cu, L, table), 70, return_lse=True)
+    check(out, lse, q, ref, cu, L, table, 0.125, True, 0, "fp16")
