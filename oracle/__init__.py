@@ -39,6 +39,9 @@ title and section):
                definitions with that batch's operands (PR #33533 commit
                messages and Speed Tests: the masked fused quant of the EP-MoE
                path; sglang PR #44861 Modifications: strided 3-D inputs).
+* ``kv``     -- RMS norm and rotation of query and key heads, the paged E4M3
+               key/value cache (write, read) and attention over it, from the
+               formulas of include/fp8sm.h.
 
 Every function states which pins in ``tests/test_oracle_*.py`` tie it to
 something other than itself.
