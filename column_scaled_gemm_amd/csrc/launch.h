@@ -190,7 +190,7 @@ struct AttnArgs {
   int few_by_seq;       // unjoined rows of `few` are [sequence][kFewRows][head], else [T][Hq]
   int row_limit;        // sequences of at most this many rows (tokens x G) are few's
 };
-constexpr int kFewRows = 64;  // row_limit where both kernels run
+constexpr int kFewRows = 32;  // most rows of a sequence that are few's (row_limit where both kernels run)
 
 struct AttnPlan {
   int few_tiles;  // 16-row tiles of a workgroup of few rows, 0: not launched
