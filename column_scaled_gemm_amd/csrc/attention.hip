@@ -827,7 +827,8 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   };
   // Steps of which this wavefront's rows see everything are a loop of their own,
   // between two that mask (one loop that picks the variant step by step moved the
-  // accumulator between registers every time).
+  // accumulator between registers every time).  Whichever loop a wavefront is in, it
+  // passes advance() once for each of the workgroup's steps, so all meet there.
   auto walk = [&](auto wide_tag) {
     auto masked = [&](int from, int to) {
       for (int i = from; i < to; ++i) {

@@ -380,7 +380,8 @@ fp8sm_status fp8sm_qk_norm_rope(const void* x, fp8sm_dtype in, int64_t T, int32_
  * left as it was and never read.
  *   k, v  device bf16/fp16 [T][ld]: Hkv heads of D values (e.g. columns of the
  *         QKV product's rows); 16-byte aligned, ld_k, ld_v multiples of 8.
- * A block written by two sequences of one call is not defined.
+ * A block that two sequences of one call write, or one sequence under two
+ * positions, is not defined.
  */
 fp8sm_status fp8sm_kv_cache_write(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
                                   fp8sm_dtype in, int64_t T, int64_t nseq, const int32_t* cu,
