@@ -142,17 +142,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _ptrs(*tensors):
-    """_ptr of each of several tensors, asking for the current device once."""
-    cur = torch.cuda.current_device() if tensors[0].is_cuda else None
-    out = []
+def _on_current(*tensors):
+    """The raw current stream, then _ptr of each of several tensors (the current
+    device is asked for once)."""
+    if not tensors[0].is_cuda:
+        _ptr(tensors[0])
+    cur = torch.cuda.current_device()
+    out = [_raw_stream(cur) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream]
     for t in tensors:
-        if t is None:
-            out.append(None)
-        elif t.get_device() == cur:
-            out.append(t.data_ptr())
-        else:
-            out.append(_ptr(t))
+        out.append(None if t is None else t.data_ptr() if t.get_device() == cur else _ptr(t))
     return out
 
 
@@ -657,6 +655,14 @@ def _head_rows(t, heads, head_dim, what):
     return sh[0], (t.stride(0) if sh[0] > 1 else heads * head_dim)
 
 
+def _out_rows(t, T, heads, head_dim, dtype, what):
+    """Row stride of an output of at least T such rows."""
+    rows, ld = _head_rows(t, heads, head_dim, what)
+    if rows < T or t.dtype != dtype:
+        raise ValueError(f"{what}: needs {T} rows of {dtype}, got {rows} of {t.dtype}")
+    return ld
+
+
 def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_weight=None,
                  k_weight=None, eps=1e-6, interleaved=False, out=None, stream=None):
     """x [T, >= (q_heads + k_heads) * head_dim] bf16/fp16, rows of query heads
@@ -665,13 +671,17 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_
     positions[t] (device int32 [T]) of cos_sin (device fp32 [positions, rot]: rot/2
     cosines, then sines; None: no rotation).  Rows at positions outside the table
     are padding and left as `out` held them.  out=x works in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_norm_rope(x, q_heads, k_heads, head_dim, positions, cos_sin, q_weight,
+                                k_weight, eps, interleaved, out)
     T = x.shape[0]
     row = (q_heads + k_heads) * head_dim
     _unit_last(x, "x")
     _holds(x, (T, row), "x")
     if out is None:
         out = torch.empty((T, row), dtype=x.dtype, device=x.device)
-    else:
+    elif out is not x:
         _unit_last(out, "out")
         _holds(out, (T, row), "out", x.dtype)
     rot = max_pos = 0
@@ -686,11 +696,10 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_
     for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None:
             _holds_bytes(t, 2 * head_dim, what, x.dtype)
-    px, pq, pk, pc, pp, po = _ptrs(x, q_weight, k_weight, cos_sin, positions, out)
+    st, px, pq, pk, pc, pp, po = _on_current(x, q_weight, k_weight, cos_sin, positions, out)
     st = _load().fp8sm_qk_norm_rope(px, _dtype_code(x), T, q_heads, k_heads, head_dim, _row_ld(x),
                                     pq, pk, eps, pc, max_pos, pp, rot,
-                                    ROPE_INTERLEAVED if interleaved else 0, po, _row_ld(out),
-                                    _stream(stream))
+                                    ROPE_INTERLEAVED if interleaved else 0, po, _row_ld(out), st)
     _check(st, "fp8sm_qk_norm_rope")
     return out
 
@@ -756,15 +765,18 @@ def kv_cache_write(k, v, cache, cu, lens, table, stream=None):
     fp16, any row stride) into the cache.  Sequence b's rows are cu[b] ..
     cu[b+1]-1 and its lens[b] cached tokens, these included, lie in the blocks
     table[b] (all device int32).  -> cache, written in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_cache_write(k, v, cache, cu, lens, table)
     P, H, D, block = _cache_args(cache)
     B, ld_table, n = _batch_args(cu, lens, table)
     T, ld_k = _head_rows(k, H, D, "k")
     Tv, ld_v = _head_rows(v, H, D, "v")
     if Tv != T or v.dtype != k.dtype:
         raise ValueError("k and v must have the same rows and dtype")
-    pk, pv, pc, pl, pt, *codes = _ptrs(k, v, cu, lens, table, *cache)
+    st, pk, pv, pc, pl, pt, *codes = _on_current(k, v, cu, lens, table, *cache)
     st = _load().fp8sm_kv_cache_write(pk, ld_k, pv, ld_v, _dtype_code(k), T, B, pc, pl, pt, ld_table,
-                                      n, P, H, D, block, *codes, _stream(stream))
+                                      n, P, H, D, block, *codes, st)
     _check(st, "fp8sm_kv_cache_write")
     return cache
 
@@ -773,19 +785,23 @@ def kv_cache_read(cache, cu, lens, table, total, dtype=torch.bfloat16, k=None, v
                   stream=None):
     """The last cu[b+1] - cu[b] cached tokens of every sequence, widened ->
     (k, v), each [total, heads, D]; total >= cu[-1], rows past it unwritten."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return kv_cache_read(cache, cu, lens, table, total, dtype, k, v)
     P, H, D, block = _cache_args(cache)
     B, ld_table, n = _batch_args(cu, lens, table)
+    ld_k = ld_v = H * D
     if k is None:
         k = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
+    else:
+        ld_k = _out_rows(k, total, H, D, dtype, "k")
     if v is None:
         v = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
-    Tk, ld_k = _head_rows(k, H, D, "k")
-    Tv, ld_v = _head_rows(v, H, D, "v")
-    if Tk < total or Tv < total or k.dtype != dtype or v.dtype != dtype:
-        raise ValueError(f"k and v need {total} rows of {dtype}")
-    pk, pv, pc, pl, pt, *codes = _ptrs(k, v, cu, lens, table, *cache)
+    else:
+        ld_v = _out_rows(v, total, H, D, dtype, "v")
+    st, pk, pv, pc, pl, pt, *codes = _on_current(k, v, cu, lens, table, *cache)
     st = _load().fp8sm_kv_cache_read(*codes, P, H, D, block, total, B, pc, pl, pt, ld_table, n,
-                                     _dtype_code(k), pk, ld_k, pv, ld_v, _stream(stream))
+                                     _dtype_code(k), pk, ld_k, pv, ld_v, st)
     _check(st, "fp8sm_kv_cache_read")
     return k, v
 
@@ -804,6 +820,10 @@ def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, c
     scale defaults to D^-1/2.  max_q >= every cu[b+1] - cu[b] and max_kv >= every
     lens[b] (default: the table's reach) only steer the choice of kernels.
     workspace: uint8, attention_cache_workspace bytes; allocated here if None."""
+    if stream is not None:  # what is allocated here belongs to that stream then
+        with torch.cuda.stream(stream):
+            return attention_cache(q, cache, cu, lens, table, max_q, max_kv, scale, causal, window,
+                                   out, lse, return_lse, workspace)
     P, H, D, block = _cache_args(cache)
     B, ld_table, n = _batch_args(cu, lens, table)
     if q.dim() != 3:
@@ -814,9 +834,7 @@ def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, c
         out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
         ld_o = Hq * D
     else:
-        To, ld_o = _head_rows(out, Hq, D, "out")
-        if To < T or out.dtype != q.dtype:
-            raise ValueError(f"out: needs {T} rows of {q.dtype}")
+        ld_o = _out_rows(out, T, Hq, D, q.dtype, "out")
     if lse is not None:
         _holds_bytes(lse, 4 * T * Hq, "lse", torch.float32)
     elif return_lse:
@@ -829,12 +847,11 @@ def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, c
         _holds_bytes(workspace, need, "workspace", torch.uint8)
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)
-    pq, pc, pl, pt, po, pe, pw, *codes = _ptrs(q, cu, lens, table, out, lse, workspace, *cache)
+    st, pq, pc, pl, pt, po, pe, pw, *codes = _on_current(q, cu, lens, table, out, lse, workspace,
+                                                         *cache)
     st = L.fp8sm_attention_cache(
         pq, ld_q, _dtype_code(q), T, B, Hq, pc, pl, pt, ld_table, n, *codes, P, H, D, block, max_q,
         max_kv, D ** -0.5 if scale is None else scale, ATTN_CAUSAL if causal else 0, window, po,
-        ld_o, pe, pw, need, _stream(stream))
+        ld_o, pe, pw, need, st)
     _check(st, "fp8sm_attention_cache")
     return (out, lse) if return_lse else out

@@ -345,3 +345,22 @@ def test_sequences_that_share_blocks():
     q = torch.from_numpy(r.standard_normal((72, 3, 64)).astype(np.float32)).to(torch.float16).cuda()
     out, lse = fp8sm.attention_cache(q, dev_cache(ref), *to_dev(cu, L, table), 70, return_lse=True)
     check(out, lse, q, ref, cu, L, table, 0.125, True, 0, "fp16")
+
+
+def test_on_a_stream_that_is_not_the_current_one():
+    """The outputs and the workspace allocated for such a call are that stream's, so
+    memory that the current stream still works on is not handed to it."""
+    got, lse, q, ref, d = run([1, 1, 2], [3000, 500, 2500], 8, 2, 128, 32, "bf16")
+    cache, side = dev_cache(ref), torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for _ in range(4):
+            busy = busy @ busy * 1e-4      # the current stream is behind, its freed memory in use
+        out = fp8sm.attention_cache(q, cache, *d, 2, stream=side)
+        k, v = fp8sm.kv_cache_read(cache, *d, 4, stream=side)
+        side.synchronize()
+        assert torch.equal(out.cpu(), got.cpu())
+        w = okv.read(ref, d[0].cpu().numpy(), d[1].cpu().numpy(), d[2].cpu().numpy(), 4)
+        assert torch.equal(k.cpu(), torch.from_numpy(w[0]).bfloat16())
+        assert torch.equal(v.cpu(), torch.from_numpy(w[1]).bfloat16())
