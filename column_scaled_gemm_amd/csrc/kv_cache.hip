@@ -224,6 +224,10 @@ __device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
   return (int)((__float_as_uint(a) + 0x1FFFFFu) >> 23) - 8;
 }
 
+// 2^-(e - 127) of a biased exponent: a block written elsewhere may hold up to 254,
+// whose factor is below the normal range
+__device__ __forceinline__ float encode_factor(int e) { return exp_byte_value(max(254 - e, 0)); }
+
 template <bool F16>
 __device__ __forceinline__ void widen2(uint32_t v, float& a, float& b) {
   if constexpr (F16) {
@@ -306,7 +310,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
     }
     m = unit_max<W>(m, red);
     const int e = max(block_exponent(m), e_old);
-    const float mult = pow2f(127 - e);
+    const float mult = encode_factor(e);
     if (!live) return;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
@@ -352,7 +356,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
       }
     m = unit_max<W>(m, red);
     const int e = max(block_exponent(m), e_old);
-    const float mult = pow2f(127 - e);
+    const float mult = encode_factor(e);
     if (!live) return;
 #pragma unroll
     for (int q = 0; q < NS; ++q) {

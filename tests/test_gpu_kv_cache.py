@@ -177,6 +177,25 @@ def test_read_of_any_exponent(byte):
             assert torch.equal(g.cpu(), w)
 
 
+@pytest.mark.parametrize("byte", [0, 246, 253, 254])
+def test_append_to_a_block_of_any_exponent(byte):
+    """A block that was written elsewhere may hold every exponent of the format."""
+    r = rng(33)
+    ref = random_cache(r, 1, 2, 16, 64)
+    for e in ref.exp:
+        e[:] = byte
+    x = r.standard_normal((4, 2, 64)).astype(np.float32)
+    x[0] = np.sign(x[0]) * np.float32(3e38)
+    x[1] *= np.float32(3e37)
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    cu, L, table = np.int32([0, 4]), np.int32([9]), np.int32([[0]])
+    dev = dev_cache(ref)
+    fp8sm.kv_cache_write(x.cuda(), x.cuda(), dev, *to_dev(cu, L, table))
+    okv.write(ref, x.double().numpy(), x.double().numpy(), cu, L, table)
+    for g, c in zip(dev, ref.codes + ref.exp):
+        assert np.array_equal(g.cpu().numpy(), c)
+
+
 def test_cache_offsets_beyond_32_bits():
     """A cache of 5 GiB a side: the blocks at its end."""
     H, D, block = 8, 128, 128
