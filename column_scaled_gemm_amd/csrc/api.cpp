@@ -643,11 +643,14 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   a.lse = lse;
   a.Hq = Hq;
   a.G = Hq / Hkv;
-  // 0 becomes the smallest normal factor, so that a masked -inf stays -inf
-  a.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+  // 0 becomes the smallest normal factor, so that a masked -inf stays -inf; none
+  // is infinite, so that a score of 0 stays 0
+  a.scale_log2 = std::min(std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN), FLT_MAX);
   a.negate = scale < 0.f;
   a.causal = (flags & FP8SM_ATTN_CAUSAL) != 0;
-  a.window = window;
+  // no sequence is longer than kMaxDim: such a window bounds nothing (and a row's
+  // position less it need not fit 32 bits)
+  a.window = window >= kMaxDim ? 0 : window;
   auto place = [&](AttnSplit sp, size_t offset) {
     sp.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + offset);
     sp.ml = sp.n > 1 ? sp.o + (size_t)sp.n * sp.rows * D : sp.o;

@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
   // runs of 16 tokens are gathered into LDS before (the plan's chunks need one
   // gather): with the block's number read just before its codes, every step waited
   // for two trips to memory (two sequences of 131072 tokens, 32 rows: 257 us, and
-  // 167 so, before the changes below and in the grid's order).
+  // 167 with the gather; the grid's odd stride and the parallel join make it 101).
   const int last_run = max((t_end - 1) >> 4, 0);
   uint4 kc[4][NI], vc[DT];
   for (int seg = t_begin; seg < t_end; seg += 16 * kFewRuns) {
@@ -1004,8 +1004,9 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
     chunk = std::max(least, (chunk + 255) / 256 * 256);
     AttnSplit s{};
     s.chunk = (int)chunk;
-    // (the grid stays within bounds whatever the hints say: the chunks grow)
-    const int64_t cap = std::max<int64_t>(1, ((int64_t)1 << 22) / std::max<int64_t>(tiles, 1));
+    // (the grid stays within bounds whatever the hints say, also with more sequences
+    // than rows, each of which has a slot: the chunks grow)
+    const int64_t cap = std::max<int64_t>(1, ((int64_t)1 << 22) / std::max(tiles, B * Hkv));
     s.n = (int)std::min(std::max<int64_t>(1, (kv + chunk - 1) / chunk), cap);
     s.rows = T * Hq;
     return s;

@@ -146,6 +146,15 @@ def test_attention_workspace():
     assert fp8sm.attention_cache_workspace(1, 1, 1, 1, 64, 1 << 62, 1 << 62) > 0
 
 
+@pytest.mark.parametrize("T,B,H", [(1, 1 << 20, 1), (1, 1 << 20, 1024), (1000, 1 << 17, 8), (64, 4096, 8)])
+def test_splits_fit_a_grid_with_more_sequences_than_rows(T, B, H):
+    """Every sequence has a slot for each head and split; a grid has 65536 x 65535."""
+    from column_scaled_gemm_amd import fp8sm
+    need = fp8sm.attention_cache_workspace(T, B, H, H, 64, 1, 1 << 30)
+    splits = max(1, need // (T * H * (64 + 2) * 4))
+    assert (T // 16 + B) * (H * splits + 1) <= 65536 * 65535
+
+
 def test_binding_refuses_what_the_abi_cannot_see():
     from column_scaled_gemm_amd import fp8sm
     c = fp8sm.kv_cache_empty(3, 2, 64, 16, device="cpu")

@@ -317,6 +317,19 @@ def test_zero_and_negative_scale(n, scale):
     assert np.all(np.abs(lse.double().cpu().numpy() - s) <= tl)
 
 
+@pytest.mark.parametrize("n", [[1, 2], [70, 1]])
+def test_largest_scale_of_scores_that_are_zero(n):
+    got, lse, *_ = run(n, [130, 70], 4, 2, 64, 16, "bf16", gain=0.0, scale=3e38)
+    assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("n,lens", [([6, 3], [2, 40]), ([140], [70])])
+@pytest.mark.parametrize("window", [(1 << 30) - 1, 1 << 30, (1 << 31) - 1])
+def test_largest_windows(n, lens, window):
+    """Rows before the first token too: their position less the window."""
+    run(n, lens, 2, 1, 64, 16, "bf16", window=window)
+
+
 @pytest.mark.parametrize("n", [[3], [80]])
 @pytest.mark.parametrize("ke,ve", [(85, 85), (100, 200), (85, 240)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
