@@ -710,6 +710,9 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
         }
       }
     uint32_t keep[2][4];
+    // most masked steps hold no token that no row sees, and no NaN code: one test each
+    // (1040 -> 1027 us; 41.0 -> 39.9 with a window of 1000 over ragged pieces)
+    const bool edge = missing || t0 < sp.lo || t0 + kManyStep > t_end;
     float mx = -INFINITY;
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
@@ -726,8 +729,9 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
           if (t + k < lo || t + k >= see_hi) sc[grp][k] = -INFINITY;
         // what no row sees may hold anything, NaN codes too
         const int vlo = none ? 0x7FFFFFFF : sp.lo;
+        if (edge)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) keep[grp][k] = token_bytes(t + 4 * k, vlo, t_end);
+          for (int k = 0; k < 4; ++k) keep[grp][k] = token_bytes(t + 4 * k, vlo, t_end);
       }
 #pragma unroll
       for (int k = 0; k < 16; ++k) mx = fmaxf(mx, sc[grp][k]);
@@ -760,7 +764,6 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
       // are found by a product of their own.
       auto clear_nan = [&](uint4& c, f32x16& od) {
         const uint32_t n0 = nan_codes(c.x), n1 = nan_codes(c.y), n2 = nan_codes(c.z), n3 = nan_codes(c.w);
-        if (!__any((n0 | n1 | n2 | n3) != 0)) return;
         const int t = t0 + 32 * grp + 16 * h;
         const int lo = mpage[mb][mi + 2 * grp + h] < 0 ? 0x7FFFFFFF : see_lo;
         f16x8 vis[2];
@@ -776,6 +779,21 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
           if (z[k] > 0.f) od[k] = __builtin_nanf("");
         c.x &= ~byte_mask(n0), c.y &= ~byte_mask(n1), c.z &= ~byte_mask(n2), c.w &= ~byte_mask(n3);
       };
+      uint4 c[DT];
+#pragma unroll
+      for (int d = 0; d < DT; ++d) c[d] = *reinterpret_cast<const uint4*>(vrow + 512 * d);
+      if constexpr (PARTIAL) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          if (edge) c[d].x &= keep[grp][0], c[d].y &= keep[grp][1], c[d].z &= keep[grp][2], c[d].w &= keep[grp][3];
+          any |= nan_codes(c[d].x) | nan_codes(c[d].y) | nan_codes(c[d].z) | nan_codes(c[d].w);
+        }
+        if (__any(any != 0)) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d) clear_nan(c[d], o[d]);
+        }
+      }
       if constexpr (WIDE) {
         bf16x8 ph[2], pl[2];
 #pragma unroll
@@ -786,12 +804,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          uint4 c = *reinterpret_cast<const uint4*>(vrow + 512 * d);
-          if constexpr (PARTIAL) {
-            c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
-            clear_nan(c, o[d]);
-          }
-          const bf16x8 v0 = widen_bf16(c.x, c.y, vs), v1 = widen_bf16(c.z, c.w, vs);
+          const bf16x8 v0 = widen_bf16(c[d].x, c[d].y, vs), v1 = widen_bf16(c[d].z, c[d].w, vs);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, ph[0], o[d], 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, pl[0], o[d], 0, 0, 0);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, ph[1], o[d], 0, 0, 0);
@@ -803,13 +816,8 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
         for (int k = 0; k < 16; ++k) p[k >> 3][k & 7] = (_Float16)sc[grp][k];
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          uint4 c = *reinterpret_cast<const uint4*>(vrow + 512 * d);
-          if constexpr (PARTIAL) {
-            c.x &= keep[grp][0], c.y &= keep[grp][1], c.z &= keep[grp][2], c.w &= keep[grp][3];
-            clear_nan(c, o[d]);
-          }
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.x, c.y, vs), p[0], o[d], 0, 0, 0);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c.z, c.w, vs), p[1], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c[d].x, c[d].y, vs), p[0], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen_f16(c[d].z, c[d].w, vs), p[1], o[d], 0, 0, 0);
         }
       }
     }
