@@ -501,12 +501,14 @@ constexpr int kMetaSteps = 32;  // steps whose runs' blocks and scales one gathe
 
 // 16-byte global -> LDS copy: reads base + off, lane i writes lds + 16 i.
 // Inline asm, so that the compiler does not wait for it before each LDS read;
-// wait_copies waits for what is needed.  m0 is used for nothing else here.
+// wait_copies waits for what is needed.  m0 is used for nothing else here; a copy
+// that follows its write needs one wait state, which inside inline asm nobody
+// else puts in.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 template <int OFF>
 __device__ __forceinline__ void copy16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3"
                :
                : "s"(lds), "v"(off), "s"(base), "n"(OFF)
                : "memory", "m0");

@@ -258,11 +258,13 @@ __device__ __attribute__((aligned(16))) uint8_t g_zero16[16];
 // kernel waits for exactly the stages it needs with wait_vmcnt.  lds_addr is
 // the wave-uniform LDS byte address of lane 0's destination; lane i writes
 // lds_addr + 16 i.
-// m0 is clobbered on purpose: these kernels use it for nothing else.
+// m0 is clobbered on purpose: these kernels use it for nothing else.  A copy that
+// follows its write needs one wait state (s_nop), which inside inline asm nobody
+// else puts in.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* g, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(lds_addr), "v"(g)
                : "memory", "m0");
@@ -306,7 +308,7 @@ __device__ __forceinline__ i32x4 sgpr_rsrc(const void* base) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16_buf(uint32_t voff, i32x4 rsrc, int soff, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory", "m0");
