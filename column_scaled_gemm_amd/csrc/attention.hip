@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
   const int b = s.b;
   const int rows = s.n * a.G;
   const int64_t r64 = (slot - s.first) * (16 * QT);
-  if (r64 >= rows || rows > a.row_limit) return;
+  if (r64 < 0 || r64 >= rows || rows > a.row_limit) return;  // (< 0: rows before the first sequence)
   const int r0 = (int)r64;
   const Span sp = row_span(a, a.few, s, r0, min(r0 + 16 * QT, rows));
   const int ns = sp.splits;
@@ -554,7 +554,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   const int b = s.b;
   const int rows = s.n * a.G;
   const int64_t r64 = (slot - s.first) * kManyRows;
-  if (r64 >= rows || rows <= a.row_limit) return;
+  if (r64 < 0 || r64 >= rows || rows <= a.row_limit) return;  // (< 0: rows before the first sequence)
   const int r0 = (int)r64;
   const Span sp = row_span(a, a.many, s, r0, min(r0 + kManyRows, rows));
   const int ns = sp.splits;

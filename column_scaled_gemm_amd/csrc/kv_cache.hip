@@ -267,6 +267,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(WriteArgs a) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int bs = a.c.block_shift, block = W * TPW;
   const Seq s = find_seq(a.kb, bs, blockIdx.x, 1, bs, 2);
+  if (blockIdx.x < s.first) return;  // a slot of rows before the first sequence
   const int start = s.len - s.n;  // position of the first new token
   const int lo = max(start, 0);   // of the first one that has a place
   const int j = (lo >> bs) + (int)(blockIdx.x - s.first);
@@ -450,6 +451,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(ReadArgs a) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Seq s = find_seq(a.kb, a.c.block_shift, blockIdx.x, 1, 4, 2);
+  if (blockIdx.x < s.first) return;  // a slot of rows before the first sequence
   const int start = s.len - s.n;
   const int H = a.c.heads;
   const int unit = blockIdx.y * 4 + w;

@@ -21,7 +21,8 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 // Work slots of a ragged batch without a plan made on the host: sequence b's
 // slots start at f(b) = floor(cu[b] * mul / 2^shift) + add * b, which leaves
 // room for n * mul / 2^shift + add of them.  Returns the sequence that owns
-// slot u (the last b with f(b) <= u).  Every lane of the wavefront takes part:
+// slot u (the last b with f(b) <= u), or sequence 0 with u < first where rows before
+// the first sequence leave slots that nobody owns.  Every lane of the wavefront takes part:
 // one round of 64 probes for up to 64 sequences, two for 4096; the last round
 // brings the sequence's other numbers along.
 // The device arrays are data, not checked by the host: whatever they hold, the

@@ -1,0 +1,52 @@
+"""Cache and attention calls at the edges of what their documentation allows:
+rows far outside the sequences, sinks, huge scales, many sequences, long walks.
+Against the 64-bit oracle, within the bounds of kv_util."""
+import numpy as np
+import pytest
+import torch
+
+from column_scaled_gemm_amd import fp8sm
+from kv_util import DT, batch, dev_cache, random_cache, rng, to_dev
+from oracle import kv as okv
+from test_gpu_attention import check
+from test_gpu_kv_cache import check_cache
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(r, T, H, D, dtype="bf16"):
+    return torch.from_numpy(r.standard_normal((T, H, D)).astype(np.float32)).to(DT[dtype])
+
+
+@pytest.mark.parametrize("before", [16, 200, 1000])
+@pytest.mark.parametrize("block", [16, 128])
+@pytest.mark.parametrize("n,lens", [([3, 90], [40, 90]), ([0, 5], [70, 300]), ([33], [33])])
+def test_many_rows_before_the_first_sequence(n, lens, block, before):
+    """More of them than a block or a tile of rows: they have work slots that no
+    sequence owns.  Nothing is written there, to no cache block either."""
+    print(f"[case] before {before} {n} {lens} {block}", flush=True)
+    r = rng(before + block)
+    H, D = 2, 64
+    cu, L, table, blocks = batch(r, n, lens, block)
+    cu = (cu + before).astype(np.int32)
+    T = int(cu[-1]) + 40
+    ref = random_cache(r, blocks, H, block, D)
+    for e in ref.exp:
+        e[:] = 40       # below what a write of nothing would set
+    x = rows(r, T, H, D)
+    dev, d = dev_cache(ref), to_dev(cu, L, table)
+    fp8sm.kv_cache_write(x.cuda(), x.cuda(), dev, *d)
+    okv.write(ref, x.double().numpy(), x.double().numpy(), cu, L, table)
+    check_cache(dev, ref)
+    got = [torch.full((T, H, D), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    fp8sm.kv_cache_read(dev, *d, T, k=got[0], v=got[1])
+    for g, w in zip(got, okv.read(ref, cu, L, table, T)):
+        assert torch.equal(g.cpu(), torch.from_numpy(np.where(np.isnan(w), 3.0, w)).to(torch.bfloat16))
+    q = rows(r, T, 4, D).cuda()
+    for max_q in (1, 16, T):        # the kernels for few and for many rows
+        out, lse = torch.full_like(q, 5.0), torch.full((T, 4), 5.0, device="cuda")
+        fp8sm.attention_cache(q, dev, *d, max_q, out=out, lse=lse)
+        mine = check(out, lse, q, ref, cu, L, table, D ** -0.5, True, 0, "bf16")
+        rest = torch.from_numpy(~mine.all((1, 2)))
+        assert int(rest.sum()) == T - sum(n)
+        assert torch.all(out.cpu()[rest] == 5) and torch.all(lse.cpu()[rest] == 5)
