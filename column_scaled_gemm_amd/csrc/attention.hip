@@ -26,9 +26,13 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 // The running maximum is moved only when a row's scores exceed it by more than
-// 2^kSlack (p <= 2^kSlack then: no precision is lost, fp16 reaches 2^15), so
-// most steps do not rescale the accumulator.
+// kSlack (p <= 2^kSlack then), so most steps do not rescale the accumulator.
 constexpr float kSlack = 8.0f;
+// Where P is rounded to fp16, a row's reference is its running maximum less kLift: p
+// <= 2^(kSlack + kLift) = 2^15, which fp16 holds, and its fixed step below 2^-14 lies
+// at 2^-31 of the row's largest p.  Without the lift it is 2^-24, and a tail 16 nats
+// below a token of small value is off by 6%, one of 18 nats lost.
+constexpr float kLift = 7.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Eight codes widened times a power of two, exactly unless the result leaves
@@ -490,7 +494,8 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
 // token 16 ((m >> 2) & 1) + 4 (m >> 3) + m % 4, so lane half h has the scores
 // of the consecutive tokens 16 h .. 16 h + 15 in its registers 0 .. 15.
 //
-// P is rounded to fp16 (half a step: 2^-11 of p) and V is widened to fp16
+// P is rounded to fp16 (half a step: 2^-11 of p, or 2^-32 of the row's largest if that
+// is more, see kLift) and V is widened to fp16
 // relative to the largest value scale within reach of the row tile: exact
 // while the scales lie within 2^15 of each other (the smallest code's last
 // bit, 2^-9, still is a fp16 value).  Wider ranges take V in bf16 and P as the
@@ -654,7 +659,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[d][k] = 0.f;
-  float m = -INFINITY, l = 0.f;  // m: in units of log2 after the scale
+  float m = -INFINITY, l = 0.f;  // m: the reference, in units of log2 after the scale
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)&ring[0][0][0]);
   // a lane's place in a copy of key rows: LDS takes them in lane order, and 16-byte
@@ -686,6 +691,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   // One step.  PARTIAL: some row does not see some of its tokens.
   auto compute = [&](int i, auto wide_tag, auto partial_tag) {
     constexpr bool WIDE = decltype(wide_tag)::value, PARTIAL = decltype(partial_tag)::value;
+    constexpr float lift = WIDE ? 0.f : kLift;
     const int t0 = t_begin + i * kManyStep;
     const uint8_t* lk = ring[i % kManySlots][0];
     const uint8_t* lv = ring[i % kManySlots][1];
@@ -739,8 +745,8 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
       for (int k = 0; k < 16; ++k) mx = fmaxf(mx, sc[grp][k]);
     }
     mx = half_max(mx) * a.scale_log2;
-    if (__any(mx > m + kSlack)) {  // (also the first finite score of a row: m = -inf)
-      const float mn = fmaxf(m, mx);
+    if (__any(mx > m + (kSlack + lift))) {  // (also the first finite score of a row: m = -inf)
+      const float mn = fmaxf(m, mx - lift);
       const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= al;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from column_scaled_gemm_amd import fp8sm
-from kv_util import DT, batch, dev_cache, random_cache, rng, to_dev
+from kv_util import DT, attention_bounds, batch, dev_cache, random_cache, rng, to_dev
 from oracle import kv as okv
 from test_gpu_attention import check
 from test_gpu_kv_cache import check_cache
@@ -50,3 +50,41 @@ def test_many_rows_before_the_first_sequence(n, lens, block, before):
         rest = torch.from_numpy(~mine.all((1, 2)))
         assert int(rest.sum()) == T - sum(n)
         assert torch.all(out.cpu()[rest] == 5) and torch.all(lse.cpu()[rest] == 5)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,ln", [(3, 200), (80, 200), (3, 2500), (80, 2500)])
+@pytest.mark.parametrize("gap", [10, 13, 16, 18, 22, 25])
+def test_a_sink_whose_value_is_zero(n, ln, gap, dtype, D):
+    """The first token leads every row by `gap` nats and adds nothing: what is left is
+    the tail.  A p may be off by half a step of fp16 (few rows of bf16 calls: of bf16)
+    or by 2^-32 of the row's largest p, whichever is more; the latter moves a result by
+    at most 2^-32 of the sum of the values' magnitudes."""
+    print(f"[case] sink {n} {ln} {gap} {dtype} {D}", flush=True)
+    r = rng(gap + ln)
+    cu, L, table, blocks = batch(r, [n], [ln], 16)
+    ref = random_cache(r, blocks, 1, 16, D)
+    ref.exp[0][:], ref.exp[1][:] = 127, 127 + 4
+    # keys: channel 0 alone counts, 1 for the sink and up to 2^-6 for the others
+    for p in range(ln):
+        page, slot = table[0, p // 16], p % 16
+        k = ref.get(0, page, slot, 0).copy()
+        k[0] = 0x38 if p == 0 else int(r.integers(0, 9))
+        ref.put(0, page, slot, 0, k)
+        v = ref.get(1, page, slot, 0) & 0x7F      # of one sign: nothing cancels
+        ref.put(1, page, slot, 0, np.zeros_like(v) if p == 0 else v)
+    q = torch.zeros(n, 2, D, dtype=DT[dtype], device="cuda")
+    q[:, :, 0] = 8.0 * gap
+    d = to_dev(cu, L, table)
+    out, lse = fp8sm.attention_cache(q, dev_cache(ref), *d, n, scale=0.125, return_lse=True)
+    o, s, spread, qk = okv.attention(q.double().cpu().numpy(), ref, cu, L, table, 0.125)
+    to, tl = attention_bounds(o, s, spread, qk, 0.125, D, ln, dtype)
+    if dtype == "bf16":
+        to -= 2.0 ** -24        # bf16 has no such floor
+    total = np.abs(okv.read(ref, [0, ln], [ln], table, ln)[1]).sum(0)
+    to += 2.0 ** -32 * total
+    err = np.abs(out.double().cpu().numpy() - o) / to
+    print(f"[bound] {err.max():.3f}", flush=True)
+    assert np.all(err <= 1)
+    assert np.all(np.abs(lse.double().cpu().numpy() - s) <= tl)
