@@ -413,8 +413,7 @@ fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
  * with window > 0 (causal only) only the `window` last of those.  A row that
  * sees nothing gets zeros and lse -inf.  Statistics and sums are fp32; the
  * probabilities are rounded for the product with V, by at most half a step of
- * bf16 (2^-8 of each) in bf16 calls and of fp16 (2^-11) in fp16 calls, or by
- * 2^-32 of the row's largest where that is more.
+ * fp16 (2^-11 of each), or by 2^-32 of the row's largest where that is more.
  *   q, o  device bf16/fp16 [T][ld]: Hq heads of D values, 16-byte aligned, ld
  *         multiples of 8.  Hq a multiple of Hkv.
  *   lse   device fp32 [T][Hq] or NULL: ln of the sum of exp(scores).

@@ -58,9 +58,9 @@ def test_many_rows_before_the_first_sequence(n, lens, block, before):
 @pytest.mark.parametrize("gap", [10, 13, 16, 18, 22, 25])
 def test_a_sink_whose_value_is_zero(n, ln, gap, dtype, D):
     """The first token leads every row by `gap` nats and adds nothing: what is left is
-    the tail.  A p may be off by half a step of fp16 (few rows of bf16 calls: of bf16)
-    or by 2^-32 of the row's largest p, whichever is more; the latter moves a result by
-    at most 2^-32 of the sum of the values' magnitudes."""
+    the tail.  A p may be off by half a step of fp16 or by 2^-32 of the row's largest p,
+    whichever is more; the latter moves a result by at most 2^-32 of the sum of the
+    values' magnitudes."""
     print(f"[case] sink {n} {ln} {gap} {dtype} {D}", flush=True)
     r = rng(gap + ln)
     cu, L, table, blocks = batch(r, [n], [ln], 16)
@@ -88,3 +88,23 @@ def test_a_sink_whose_value_is_zero(n, ln, gap, dtype, D):
     print(f"[bound] {err.max():.3f}", flush=True)
     assert np.all(err <= 1)
     assert np.all(np.abs(lse.double().cpu().numpy() - s) <= tl)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,ln", [(1, 2), (2, 3), (3, 5), (2, 40), (5, 9), (40, 40), (33, 70)])
+def test_probabilities_of_bf16_calls_lose_no_more_than_fp16_keeps(n, ln, D):
+    """Values that cancel: what P was rounded by shows beside a small result's own
+    rounding.  The bound of an fp16 call, with a half step of bf16 for the result."""
+    print(f"[case] cancel {n} {ln} {D}", flush=True)
+    r = rng(n * 100 + ln)
+    G = 4       # up to 8 tokens: the kernel for few rows, more: for many
+    cu, L, table, blocks = batch(r, [n], [ln], 16)
+    ref = random_cache(r, blocks, 1, 16, D, spread=1)
+    q = (rows(r, n, G, D) * 0.05).to(torch.bfloat16).cuda()
+    out, lse = fp8sm.attention_cache(q, dev_cache(ref), *to_dev(cu, L, table), n, return_lse=True)
+    o, s, spread, qk = okv.attention(q.double().cpu().numpy(), ref, cu, L, table, D ** -0.5)
+    to, tl = attention_bounds(o, s, spread, qk, D ** -0.5, D, ln, "fp16")
+    to += 1.01 * np.abs(o) * (2.0 ** -8 - 2.0 ** -11)
+    err = np.abs(out.double().cpu().numpy() - o) / to
+    print(f"[bound] {err.max():.3f}", flush=True)
+    assert np.all(err <= 1) and np.all(np.abs(lse.double().cpu().numpy() - s) <= tl)
