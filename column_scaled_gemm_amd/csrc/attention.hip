@@ -4,8 +4,10 @@
 //
 // over the cached tokens t that row r sees: all of its sequence's, up to its
 // own position (causal), at most `window` of them.  One pass over the tokens
-// with a running maximum m and sum l in fp32 (in units of log2, so the
-// exponential is the hardware's 2^x).
+// with a running maximum m and sum l in fp32 (p = 2^((s - m) scale log2(e)), the
+// exponential being the hardware's 2^x).  Maxima are held as scores, before the
+// scale: differences of scores are then right however large the scale is, where
+// rounding m scale would move every exponent by up to half a step of it.
 //
 // The query heads that share a key head are extra rows: row r of a sequence is
 // token r / G and head r % G of its G query heads, so both kernels read each
@@ -28,11 +30,14 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 // The running maximum is moved only when a row's scores exceed it by more than
 // kSlack (p <= 2^kSlack then), so most steps do not rescale the accumulator.
 constexpr float kSlack = 8.0f;
-// Where P is rounded to fp16, a row's reference is its running maximum less kLift: p
-// <= 2^(kSlack + kLift) = 2^15, which fp16 holds, and its fixed step below 2^-14 lies
-// at 2^-31 of the row's largest p.  Without the lift it is 2^-24, and a tail 16 nats
-// below a token of small value is off by 6%, one of 18 nats lost.
-constexpr float kLift = 7.0f;
+// Where P is rounded to fp16 it is taken 2^kLift times as large: p <= 2^(kSlack +
+// kLift) = 2^15, which fp16 holds, and its fixed step below 2^-14 lies at 2^-31 of the
+// row's largest p.  Without the lift it is 2^-24, and a tail 16 nats below a token of
+// small value is off by 6%, one of 18 nats lost.
+constexpr float kLift = 7.0f, kUnlift = 1.0f / 128;
+// Up to here m scale rounds by at most 2^-4 and serves as the exponents' reference in one
+// fma; beyond, scores are subtracted first.
+constexpr float kFarScore = 1 << 20;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Eight codes widened times a power of two, exactly unless the result leaves
@@ -339,10 +344,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx = fmaxf(mx, sc[i][t][k]);
-        mx = quarter_max(mx) * a.scale_log2;
-        if (__any(mx > m[i] + kSlack)) {  // (also a row's first score: m = -inf)
+        mx = quarter_max(mx);
+        if (__any((mx - m[i]) * a.scale_log2 > kSlack)) {  // (also a row's first score: m = -inf)
           const float mn = fmaxf(m[i], mx);
-          const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[i] - mn);
+          const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[i] - mn) * a.scale_log2);
           m[i] = mn;
           l[i] *= al;
 #pragma unroll
@@ -356,7 +361,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][t][k], a.scale_log2, -ms));
+            const float p = __builtin_amdgcn_exp2f((sc[i][t][k] - ms) * a.scale_log2);
             sum += p;
             const __bf16 hi = (__bf16)p;
             ph[i][t >> 1][4 * (t & 1) + k] = hi;
@@ -447,7 +452,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
     float ll = 0.f, acc[8] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float f = __builtin_amdgcn_exp2f(sm[k][row] - ms);
+      const float f = __builtin_amdgcn_exp2f((sm[k][row] - ms) * a.scale_log2);
       ll = __builtin_fmaf(sl[k][row], f, ll);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(so[k][row][d + e], f, acc[e]);
@@ -461,7 +466,7 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
       for (int e = 0; e < 4; ++e)
         u[e] = (uint32_t)round16<F16>(acc[2 * e] * inv) | (uint32_t)round16<F16>(acc[2 * e + 1] * inv) << 16;
       *reinterpret_cast<uint4*>(a.out + t * a.ld_o + head * D + d) = make_uint4(u[0], u[1], u[2], u[3]);
-      if (a.lse && d == 0) a.lse[t * a.Hq + head] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+      if (a.lse && d == 0) a.lse[t * a.Hq + head] = __builtin_fmaf(mm, a.scale_log2, __builtin_amdgcn_logf(ll)) * kLn2;
     } else {
       const int64_t at = split * a.few.rows + part_row(a, true, b, r, t, head);
       float* po = a.few.o + at * D + d;
@@ -660,7 +665,8 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[d][k] = 0.f;
-  float m = -INFINITY, l = 0.f;  // m: the reference, in units of log2 after the scale
+  float m = -INFINITY, l = 0.f, from = 0.f;  // from: m scale - lift, the exponents' reference
+  bool far = false;                          // (of some row of the wavefront: kFarScore)
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)&ring[0][0][0]);
   // a lane's place in a copy of key rows: LDS takes them in lane order, and 16-byte
@@ -745,18 +751,27 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) mx = fmaxf(mx, sc[grp][k]);
     }
-    mx = half_max(mx) * a.scale_log2;
-    if (__any(mx > m + (kSlack + lift))) {  // (also the first finite score of a row: m = -inf)
-      const float mn = fmaxf(m, mx - lift);
-      const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+    mx = half_max(mx);
+    if (__any((mx - m) * a.scale_log2 > kSlack)) {  // (also the first finite score of a row: m = -inf)
+      const float mn = fmaxf(m, mx);
+      const float al = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * a.scale_log2);
       m = mn;
       l *= al;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[d][k] *= al;
+      from = __builtin_fmaf(m == -INFINITY ? 0.f : m, a.scale_log2, -lift);
+      far = __any(fabsf(from) >= kFarScore);
+      if (far) from = -lift;
     }
-    const float ms = m == -INFINITY ? 0.f : m;
+    if (far) {
+      const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int grp = 0; grp < 2; ++grp)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sc[grp][k] -= ms;
+    }
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
       const float vs = mvs[mb][mi + 2 * grp + h];
@@ -764,7 +779,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
       float sum = 0.f;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        sc[grp][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[grp][k], a.scale_log2, -ms));
+        sc[grp][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[grp][k], a.scale_log2, -from));
         sum += sc[grp][k];
       }
       l += sum;
@@ -882,11 +897,11 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
   }
   {
     const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
-    l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
+    l = (__uint_as_float(sw[0]) + __uint_as_float(sw[1])) * (wide ? 1.f : kUnlift);
   }
   if (!ok) return;
   const int64_t t = s.c0 + tok;
-  const float vref = wide ? 1.f : exp_byte_value(eref);
+  const float vref = wide ? 1.f : exp_byte_value(eref) * kUnlift;
   if (ns <= 1) {
     const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
     uint16_t* dst = a.out + t * a.ld_o + head * D;
@@ -901,7 +916,7 @@ __global__ __launch_bounds__(256, 2) void attn_many_kernel(AttnArgs a) {
                  (uint32_t)round16<F16>(o[d][4 * v + 2 * e + 1] * inv * vref) << 16;
         *reinterpret_cast<uint2*>(dst + 32 * d + 8 * v + 4 * h) = make_uint2(u[0], u[1]);
       }
-    if (a.lse && h == 0) a.lse[t * a.Hq + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && h == 0) a.lse[t * a.Hq + head] = __builtin_fmaf(m, a.scale_log2, __builtin_amdgcn_logf(l)) * kLn2;
   } else {
     const int64_t at = split * a.many.rows + part_row(a, false, b, r, t, head);
 #pragma unroll
@@ -960,14 +975,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int few_rows
 #pragma unroll
       for (int u = 0; u < U; ++u) mn = fmaxf(mn, ml[u].x);
       const float ms = mn == -INFINITY ? 0.f : mn;
-      const float al = __builtin_amdgcn_exp2f(m - ms);
+      const float al = __builtin_amdgcn_exp2f((m - ms) * a.scale_log2);
       m = mn;
       l *= al;
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] *= al;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float f = __builtin_amdgcn_exp2f(ml[u].x - ms);
+        const float f = __builtin_amdgcn_exp2f((ml[u].x - ms) * a.scale_log2);
         if (i0 + u * NG >= ns) continue;
         l = __builtin_fmaf(ml[u].y, f, l);
 #pragma unroll
@@ -987,7 +1002,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int few_rows
   acc = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
-    const float f = __builtin_amdgcn_exp2f(sm[gw + k] - ms);
+    const float f = __builtin_amdgcn_exp2f((sm[gw + k] - ms) * a.scale_log2);
     ll = __builtin_fmaf(sl[gw + k], f, ll);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(so[gw + k][c][e], f, acc[e]);
@@ -996,7 +1011,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int few_rows
   const uint32_t u0 = (uint32_t)round16<F16>(acc[0] * inv) | (uint32_t)round16<F16>(acc[1] * inv) << 16;
   const uint32_t u1 = (uint32_t)round16<F16>(acc[2] * inv) | (uint32_t)round16<F16>(acc[3] * inv) << 16;
   *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.ld_o + head * D + 4 * c) = make_uint2(u0, u1);
-  if (a.lse && c == 0) a.lse[id] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+  if (a.lse && c == 0) a.lse[id] = __builtin_fmaf(mm, a.scale_log2, __builtin_amdgcn_logf(ll)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------

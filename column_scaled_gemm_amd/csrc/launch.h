@@ -167,7 +167,7 @@ hipError_t launch_kv_read(const KvBatch& kb, const KvCache& c, void* k, void* v,
 
 // How one of the two attention kernels splits the cached tokens of its rows:
 // `n` splits at most, of `chunk` tokens.  Unjoined results: o [n][rows][D] and ml
-// [n][rows][2] (maximum, sum).
+// [n][rows][2] (largest score before the scale, sum).
 struct AttnSplit {
   int n, chunk;
   int64_t rows;

@@ -108,3 +108,41 @@ def test_probabilities_of_bf16_calls_lose_no_more_than_fp16_keeps(n, ln, D):
     err = np.abs(out.double().cpu().numpy() - o) / to
     print(f"[bound] {err.max():.3f}", flush=True)
     assert np.all(err <= 1) and np.all(np.abs(lse.double().cpu().numpy() - s) <= tl)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,ln", [(3, 200), (80, 200), (3, 2500), (80, 2500)])
+@pytest.mark.parametrize("scale", [3e4, 1e9, -1e9, 1e20, 3e38])
+def test_huge_scales_pick_the_largest_score(n, ln, scale, dtype, D):
+    """Scores are whole numbers, 28672 and a place in a permutation more: the softmax
+    of such scales is the token with the largest, its value comes out as it is."""
+    print(f"[case] huge {n} {ln} {scale} {dtype} {D}", flush=True)
+    r = rng(ln + n)
+    cu, L, table, blocks = batch(r, [n], [ln], 16)
+    ref = random_cache(r, blocks, 1, 16, D, spread=1)
+    ref.exp[0][:] = 127
+    codes = torch.arange(16.0).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    order = r.permutation(ln)
+    for p in range(ln):
+        k = np.zeros(D, dtype=np.uint8)
+        k[:3] = codes[order[p] % 16], codes[order[p] // 16 % 16], codes[order[p] // 256]
+        k[3] = 0x7E                                   # 448
+        ref.put(0, table[0, p // 16], p % 16, 0, k)
+    q = torch.zeros(n, 2, D, dtype=DT[dtype], device="cuda")
+    q[:, :, :4] = torch.tensor([1.0, 16.0, 256.0, 64.0])
+    d = to_dev(cu, L, table)
+    out, lse = fp8sm.attention_cache(q, dev_cache(ref), *d, n, scale=scale, return_lse=True)
+    vals = okv.read(ref, [0, ln], [ln], table, ln)[1][:, 0]
+    g, gl = out.cpu(), lse.double().cpu().numpy()
+    for i in range(n):
+        seen = order[:ln - n + 1 + i]
+        best = int(np.argmax(seen) if scale > 0 else np.argmin(seen))
+        want = torch.from_numpy(vals[best]).to(DT[dtype])
+        assert torch.equal(g[i, 0], want) and torch.equal(g[i, 1], want), i
+        top = (28672.0 + seen[best]) * scale
+        if abs(top) < 3e38:
+            # the scale, log2(e), their product, its product, ln(2) and the last one
+            assert np.all(np.abs(gl[i] - top) <= 1.01 * 6 * 2.0 ** -24 * abs(top))
+        else:
+            assert np.all(np.isposinf(gl[i]))
