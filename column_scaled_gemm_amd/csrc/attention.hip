@@ -1016,6 +1016,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int few_rows
 
 // ---------------------------------------------------------------------------
 // The plan, from sizes alone (the lengths are on the device).
+
+// Most bytes of unjoined results of one kernel.  512 sequences of one token, 64 heads
+// of 128, may have 15 splits then, of 2048 tokens or more; without a bound a reach of
+// 131072 tokens took 1 GiB, and 2^20 tokens of 1024 sequences 16.
+constexpr int64_t kMostWorkspace = (int64_t)1 << 28;
+
 AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv,
                         int64_t window) {
   const int64_t G = Hq / Hkv;
@@ -1030,7 +1036,7 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
   };
   // tokens a split: `most`, or less to make 512 workgroups (two a CU), but not
   // below `least`
-  const auto split = [&](int64_t tiles, int64_t kv, int64_t least, int64_t most) {
+  const auto split = [&](int64_t tiles, int64_t kv, int64_t least, int64_t most, int64_t rows) {
     const int64_t ns = std::max<int64_t>(1, 512 / std::max<int64_t>(tiles, 1));
     int64_t chunk = std::min((kv + ns - 1) / ns, most);
     chunk = std::max(least, (chunk + 255) / 256 * 256);
@@ -1038,9 +1044,12 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
     s.chunk = (int)chunk;
     // (the grid stays within bounds whatever the hints say, also with more sequences
     // than rows, each of which has a slot: the chunks grow)
-    const int64_t cap = std::max<int64_t>(1, ((int64_t)1 << 22) / std::max(tiles, B * Hkv));
+    int64_t cap = std::max<int64_t>(1, ((int64_t)1 << 22) / std::max(tiles, B * Hkv));
+    // (and so does the workspace: a large batch of long contexts fills the chip with
+    // fewer splits)
+    cap = std::min(cap, std::max<int64_t>(1, kMostWorkspace / (rows * (D + 2) * (int64_t)sizeof(float))));
     s.n = (int)std::min(std::max<int64_t>(1, (kv + chunk - 1) / chunk), cap);
-    s.rows = T * Hq;
+    s.rows = rows;
     return s;
   };
   p.few_split = p.many_split = AttnSplit{1, 256, T * Hq, nullptr, nullptr};
@@ -1053,7 +1062,7 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
   p.row_limit = 0;
   if (p.many) {
     const int64_t tiles = std::max(T * G / kManyRows, std::min(B, T)) * Hkv;
-    p.many_split = split(tiles, reach(kManyRows), 512, 1 << 30);
+    p.many_split = split(tiles, reach(kManyRows), 512, 1 << 30, T * Hq);
   }
   // The short sequences of a mixed batch: the kernel for many rows computes them
   // in passing where they see few tokens; with more, one workgroup of it would be
@@ -1071,11 +1080,9 @@ AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t ma
     p.row_limit = p.many ? kFewRows : 0x7FFFFFFF;
     const int64_t few_T = p.many ? std::min(B, T) : T;
     const int64_t tiles = std::max(few_T * G / (16 * p.few_tiles), std::min(B, T)) * Hkv;
-    p.few_split = split(tiles, reach(16 * p.few_tiles), 1024, p.few_tiles == 1 ? 2048 : 4096);
-    if (p.many && B * kFewRows * Hkv < T * Hq) {
-      p.few_by_seq = true;
-      p.few_split.rows = B * kFewRows * Hkv;
-    }
+    p.few_by_seq = p.many && B * kFewRows * Hkv < T * Hq;
+    p.few_split = split(tiles, reach(16 * p.few_tiles), 1024, p.few_tiles == 1 ? 2048 : 4096,
+                        p.few_by_seq ? B * kFewRows * Hkv : T * Hq);
   }
   return p;
 }

@@ -421,8 +421,9 @@ fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
  *         for speed only: they choose kernels and splits, any values give a
  *         correct result.
  *   workspace  device, 16-byte aligned, fp8sm_attention_cache_workspace bytes
- *         of the same sizes (may be 0: NULL).  Not kept between calls; calls
- *         that may run at the same time need one each.
+ *         of the same sizes (may be 0: NULL; below 512 MiB whatever the sizes).
+ *         Not kept between calls; calls that may run at the same time need one
+ *         each.
  * Further errors: workspace_bytes too small -> ERR_SHAPE; window without
  * causal, unknown flags -> ERR_UNSUPPORTED; window < 0, Hq % Hkv, a scale that is
  * not finite -> ERR_SHAPE;

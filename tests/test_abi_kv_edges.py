@@ -1,0 +1,27 @@
+"""Cache and attention calls at the edges of what their documentation allows, as
+far as the host decides them (no GPU needed)."""
+import os
+
+import pytest
+
+from conftest import ROOT
+
+LIB = os.path.join(ROOT, "column_scaled_gemm_amd", "libfp8sm.so")
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libfp8sm.so not built")
+
+
+@pytest.mark.parametrize("B,T,Hq,H,D,max_q,max_kv", [
+    (512, 512, 64, 8, 128, 1, 131072), (1024, 1024, 64, 8, 128, 1, 131072), (1024, 1024, 64, 8, 128, 1, 1 << 20),
+    (256, 2048, 64, 8, 128, 8, 1 << 30), (4096, 4096, 128, 8, 64, 1, 1 << 20), (64, 1 << 20, 64, 8, 128, 1 << 14, 1 << 20),
+    (1 << 16, 1 << 20, 8, 8, 128, 4096, 1 << 30), (1, 1, 1024, 1024, 128, 1, 1 << 30), (1, 1 << 20, 1024, 8, 128, 33, 1 << 30)])
+def test_workspace_is_bounded(B, T, Hq, H, D, max_q, max_kv):
+    from column_scaled_gemm_amd import fp8sm
+    for window in (0, 4096, (1 << 31) - 1):
+        assert fp8sm.attention_cache_workspace(T, B, Hq, H, D, max_q, max_kv, window) < 512 << 20
+
+
+def test_workspace_of_few_rows_is_that_of_their_splits():
+    from column_scaled_gemm_amd import fp8sm
+    row = (128 + 2) * 4
+    assert fp8sm.attention_cache_workspace(8, 2, 64, 8, 128, 4, 131072) == 32 * 8 * 64 * row
+    assert fp8sm.attention_cache_workspace(64, 64, 32, 8, 128, 1, 16384) == 8 * 64 * 32 * row

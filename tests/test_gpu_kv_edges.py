@@ -146,3 +146,38 @@ def test_huge_scales_pick_the_largest_score(n, ln, scale, dtype, D):
             assert np.all(np.abs(gl[i] - top) <= 1.01 * 6 * 2.0 ** -24 * abs(top))
         else:
             assert np.all(np.isposinf(gl[i]))
+
+
+def sampled(q, got, lse, cache, ref, L, table, picks, dtype="bf16", n=1, window=0):
+    """Checks the sequences `picks` of a batch of n rows each against the oracle."""
+    D = q.shape[2]
+    for b in picks:
+        sl = slice(b * n, (b + 1) * n)
+        check(got[sl], lse[sl], q[sl], ref, np.int32([0, n]), L[b:b + 1], table[b:b + 1], D ** -0.5, True, window,
+              dtype)
+
+
+@pytest.mark.parametrize("max_q,G", [(1, 4), (100, 4)])
+@pytest.mark.parametrize("long", [False, True])
+def test_more_workgroups_than_a_grids_first_dimension(max_q, G, long):
+    """70000 sequences of one row that share their blocks, for the kernels for few and
+    for many rows; the long ones in the few splits that the workspace's bound leaves,
+    with a join of more than 65536 workgroups."""
+    print(f"[case] grid {max_q} {G} {long}", flush=True)
+    r = rng(60)
+    B, D, block = 70000, 64, 128
+    top = 7000 if long else 60
+    L = r.integers(1, top + 1, B).astype(np.int32)
+    L[[0, 1, B - 2, B - 1]] = [1, top, top, 1]
+    ref = random_cache(r, 60, 1, block, D)
+    table = np.broadcast_to(r.permutation(60)[:-(-top // block)].astype(np.int32), (B, -(-top // block)))
+    cache = dev_cache(ref)
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    dl, dt = to_dev(L, table)
+    q = torch.randn(B, G, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
+    max_kv = 1 << 20 if max_q == 1 else 1000       # (beside long contexts few rows go to their own kernel)
+    need = fp8sm.attention_cache_workspace(B, B, G, 1, D, max_q, max_kv)
+    assert need == (3 * B * G * (D + 2) * 4 if max_q == 1 else 0)
+    out, lse = fp8sm.attention_cache(q, cache, cu, dl, dt, max_q, max_kv=max_kv, return_lse=True)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    sampled(q, out, lse, cache, ref, L, table, [0, 1, 40000, 65535, 65536, B - 2, B - 1])
