@@ -697,9 +697,12 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_
         if t is not None:
             _holds_bytes(t, 2 * head_dim, what, x.dtype)
     st, px, pq, pk, pc, pp, po = _on_current(x, q_weight, k_weight, cos_sin, positions, out)
-    st = _load().fp8sm_qk_norm_rope(px, _dtype_code(x), T, q_heads, k_heads, head_dim, _row_ld(x),
+    ld_x, ld_y = _row_ld(x), _row_ld(out)
+    if T <= 1 and po == px:  # in place: one stride, also where none is used
+        ld_x = ld_y = max(ld_x, ld_y)
+    st = _load().fp8sm_qk_norm_rope(px, _dtype_code(x), T, q_heads, k_heads, head_dim, ld_x,
                                     pq, pk, eps, pc, max_pos, pp, rot,
-                                    ROPE_INTERLEAVED if interleaved else 0, po, _row_ld(out), st)
+                                    ROPE_INTERLEAVED if interleaved else 0, po, ld_y, st)
     _check(st, "fp8sm_qk_norm_rope")
     return out
 

@@ -181,3 +181,19 @@ def test_more_workgroups_than_a_grids_first_dimension(max_q, G, long):
     out, lse = fp8sm.attention_cache(q, cache, cu, dl, dt, max_q, max_kv=max_kv, return_lse=True)
     assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
     sampled(q, out, lse, cache, ref, L, table, [0, 1, 40000, 65535, 65536, B - 2, B - 1])
+
+
+@pytest.mark.parametrize("T", [0, 1, 2])
+@pytest.mark.parametrize("own", [False, True])
+def test_rotation_in_place_of_few_rows(T, own):
+    """out: x itself, or the view of its query and key heads (a decode batch may
+    shrink to one row, whose stride says nothing)."""
+    r = rng(70)
+    Hq, Hk, D = 4, 2, 64
+    x = rows(r, T, Hq + 2 * Hk, D).flatten(1).cuda()
+    pos, cs = to_dev(np.arange(5, 5 + T, dtype=np.int32), np.ones((9, D), dtype=np.float32))
+    want = fp8sm.qk_norm_rope(x, Hq, Hk, D, pos, cs)
+    y = x.clone()
+    out = y if own else y[:, :(Hq + Hk) * D]
+    assert fp8sm.qk_norm_rope(y, Hq, Hk, D, pos, cs, out=out) is out
+    assert torch.equal(y[:, :(Hq + Hk) * D], want) and torch.equal(y[:, (Hq + Hk) * D:], x[:, (Hq + Hk) * D:])
