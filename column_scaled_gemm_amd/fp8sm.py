@@ -809,10 +809,16 @@ def kv_cache_read(cache, cu, lens, table, total, dtype=torch.bfloat16, k=None, v
     return k, v
 
 
+def _window(window):
+    """A window as the ABI's 32-bit number (ctypes would cut off what does not fit):
+    the largest one bounds nothing, -1 is refused."""
+    return max(-1, min(window, (1 << 31) - 1))
+
+
 def attention_cache_workspace(T, nseq, q_heads, kv_heads, head_dim, max_q, max_kv, window=0):
     """Bytes of workspace of an attention_cache call of these sizes."""
     return _load().fp8sm_attention_cache_workspace(T, nseq, q_heads, kv_heads, head_dim, max_q,
-                                                   max_kv, window)
+                                                   max_kv, _window(window))
 
 
 def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, causal=True,
@@ -844,6 +850,7 @@ def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, c
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     if max_kv is None:
         max_kv = n * block
+    window = _window(window)
     L = _load()
     need = L.fp8sm_attention_cache_workspace(T, B, Hq, H, D, max_q, max_kv, window)
     if workspace is not None:

@@ -25,3 +25,18 @@ def test_workspace_of_few_rows_is_that_of_their_splits():
     row = (128 + 2) * 4
     assert fp8sm.attention_cache_workspace(8, 2, 64, 8, 128, 4, 131072) == 32 * 8 * 64 * row
     assert fp8sm.attention_cache_workspace(64, 64, 32, 8, 128, 1, 16384) == 8 * 64 * 32 * row
+
+
+@pytest.mark.parametrize("window,means", [(1 << 31, 0), ((1 << 32) + 5, 0), (1 << 62, 0), (1 << 64, 0), ((1 << 31) - 1, 0),
+                                          (100, 100)])
+def test_windows_beyond_32_bits_bound_nothing(window, means):
+    """ctypes would cut them to their lowest bits, 5 tokens for 2^32 + 5."""
+    from column_scaled_gemm_amd import fp8sm
+    sizes = (8, 2, 64, 8, 128, 4, 131072)
+    assert fp8sm.attention_cache_workspace(*sizes, window) == fp8sm.attention_cache_workspace(*sizes, means)
+
+
+def test_negative_windows_are_refused_whatever_their_size():
+    from column_scaled_gemm_amd import fp8sm
+    assert [fp8sm._window(w) for w in (-1, -(1 << 31), -(1 << 32), -(1 << 40) + 3)] == [-1] * 4
+    assert fp8sm.attention_cache_workspace(8, 2, 64, 8, 128, 4, 131072, -(1 << 32)) == 0

@@ -8,7 +8,7 @@ import torch
 from column_scaled_gemm_amd import fp8sm
 from kv_util import DT, attention_bounds, batch, dev_cache, random_cache, rng, to_dev
 from oracle import kv as okv
-from test_gpu_attention import check
+from test_gpu_attention import check, run
 from test_gpu_kv_cache import check_cache
 
 pytestmark = pytest.mark.gpu
@@ -197,3 +197,9 @@ def test_rotation_in_place_of_few_rows(T, own):
     out = y if own else y[:, :(Hq + Hk) * D]
     assert fp8sm.qk_norm_rope(y, Hq, Hk, D, pos, cs, out=out) is out
     assert torch.equal(y[:, :(Hq + Hk) * D], want) and torch.equal(y[:, (Hq + Hk) * D:], x[:, (Hq + Hk) * D:])
+
+
+@pytest.mark.parametrize("n", [[3, 1], [80, 1]])
+@pytest.mark.parametrize("window", [(1 << 31) + 2, (1 << 32) + 5])
+def test_windows_beyond_32_bits(n, window):
+    run(n, [130, 70], 2, 1, 64, 16, "bf16", window=window)
