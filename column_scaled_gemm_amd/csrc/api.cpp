@@ -620,13 +620,14 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   fp8sm_status st = kv_args(T, nseq, cu, lens, table, ld_table, max_blocks, k_codes, v_codes,
                             k_exp, v_exp, num_blocks, Hkv, D, block, &a.kb, &a.c);
   if (st != FP8SM_OK) return st;
-  if (Hq < 1 || Hq % Hkv || window < 0 || max_q < 1 || max_kv < 0 || !std::isfinite(scale))
+  const bool empty = T == 0 || nseq == 0;
+  if (Hq < 1 || Hq % Hkv || window < 0 || max_q < (empty ? 0 : 1) || max_kv < 0 || !std::isfinite(scale))
     return FP8SM_ERR_SHAPE;
   if (window > 0 && !(flags & FP8SM_ATTN_CAUSAL)) return FP8SM_ERR_UNSUPPORTED;
   if (Hq > kMaxHeads || T * Hq > kMaxDim) return FP8SM_ERR_RANGE;
   if (ld_q < (int64_t)Hq * D || ld_o < (int64_t)Hq * D) return FP8SM_ERR_SHAPE;
   if (ld_q % 8 || ld_o % 8) return FP8SM_ERR_ALIGN;
-  if (T == 0 || nseq == 0) return FP8SM_OK;
+  if (empty) return FP8SM_OK;
   if (!q || !o) return FP8SM_ERR_NULL;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return FP8SM_ERR_ALIGN;
   const AttnPlan p = plan_attention(T, nseq, Hq, Hkv, D, max_q, max_kv, window);

@@ -417,9 +417,9 @@ fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
  *   q, o  device bf16/fp16 [T][ld]: Hq heads of D values, 16-byte aligned, ld
  *         multiples of 8.  Hq a multiple of Hkv.
  *   lse   device fp32 [T][Hq] or NULL: ln of the sum of exp(scores).
- *   max_q, max_kv  host's knowledge of max n_b (>= 1) and max lens[b] (>= 0),
- *         for speed only: they choose kernels and splits, any values give a
- *         correct result.
+ *   max_q, max_kv  host's knowledge of max n_b (>= 1, or 0 with T == 0 or nseq
+ *         == 0) and max lens[b] (>= 0), for speed only: they choose kernels and
+ *         splits, any values give a correct result.
  *   workspace  device, 16-byte aligned, fp8sm_attention_cache_workspace bytes
  *         of the same sizes (may be 0: NULL; below 512 MiB whatever the sizes).
  *         Not kept between calls; calls that may run at the same time need one

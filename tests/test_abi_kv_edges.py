@@ -40,3 +40,12 @@ def test_negative_windows_are_refused_whatever_their_size():
     from column_scaled_gemm_amd import fp8sm
     assert [fp8sm._window(w) for w in (-1, -(1 << 31), -(1 << 32), -(1 << 40) + 3)] == [-1] * 4
     assert fp8sm.attention_cache_workspace(8, 2, 64, 8, 128, 4, 131072, -(1 << 32)) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(T=0), dict(B=0), dict(T=0, B=0)])
+def test_an_empty_batch_has_no_longest_sequence(kw):
+    from test_abi_kv import _attn, _codes
+    lib, E = _codes()
+    assert _attn(lib, mq=0, mkv=0, **kw) == E["OK"]
+    assert _attn(lib, mq=-1, **kw) == _attn(lib, mkv=-1, **kw) == E["ERR_SHAPE"]
+    assert _attn(lib, mq=0) == E["ERR_SHAPE"]

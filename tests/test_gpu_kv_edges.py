@@ -203,3 +203,21 @@ def test_rotation_in_place_of_few_rows(T, own):
 @pytest.mark.parametrize("window", [(1 << 31) + 2, (1 << 32) + 5])
 def test_windows_beyond_32_bits(n, window):
     run(n, [130, 70], 2, 1, 64, 16, "bf16", window=window)
+
+
+@pytest.mark.parametrize("T,B", [(0, 2), (0, 0), (3, 0)])
+def test_empty_batches(T, B):
+    """As a server's step may leave them: no rows, no sequences, and no longest one."""
+    c = fp8sm.kv_cache_empty(3, 2, 64, 16)
+    for t in c:
+        t.fill_(7)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cu, lens, table = torch.zeros(B + 1, **i32), torch.full((B,), 20, **i32), torch.zeros(B, 2, **i32)
+    q = torch.full((T, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    k = q[:, :2].contiguous()
+    out, lse = torch.full_like(q, 5.0), torch.full((T, 4), 5.0, device="cuda")
+    fp8sm.kv_cache_write(k, k, c, cu, lens, table)
+    fp8sm.attention_cache(q, c, cu, lens, table, 0, out=out, lse=lse)
+    got = fp8sm.kv_cache_read(c, cu, lens, table, T, k=torch.full_like(k, 5.0), v=torch.full_like(k, 5.0))
+    for t, v in [(t, 7) for t in c] + [(t, 5) for t in (out, lse, *got)]:
+        assert bool(torch.all(t == v))
