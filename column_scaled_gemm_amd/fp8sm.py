@@ -785,26 +785,31 @@ def kv_cache_write(k, v, cache, cu, lens, table, stream=None):
 
 
 def kv_cache_read(cache, cu, lens, table, total, dtype=torch.bfloat16, k=None, v=None,
-                  stream=None):
+                  stream=None, keys=True, values=True):
     """The last cu[b+1] - cu[b] cached tokens of every sequence, widened ->
-    (k, v), each [total, heads, D]; total >= cu[-1], rows past it unwritten."""
+    (k, v), each [total, heads, D]; total >= cu[-1], rows past it unwritten.
+    keys=False or values=False reads the other alone, with None in its place."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return kv_cache_read(cache, cu, lens, table, total, dtype, k, v)
+            return kv_cache_read(cache, cu, lens, table, total, dtype, k, v, None, keys, values)
     P, H, D, block = _cache_args(cache)
     B, ld_table, n = _batch_args(cu, lens, table)
+    if (k is not None and not keys) or (v is not None and not values):
+        raise ValueError("k with keys=False, or v with values=False")
     ld_k = ld_v = H * D
-    if k is None:
-        k = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
-    else:
+    if k is not None:
         ld_k = _out_rows(k, total, H, D, dtype, "k")
-    if v is None:
-        v = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
-    else:
+    elif keys:
+        k = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
+    if v is not None:
         ld_v = _out_rows(v, total, H, D, dtype, "v")
-    st, pk, pv, pc, pl, pt, *codes = _on_current(k, v, cu, lens, table, *cache)
+    elif values:
+        v = torch.empty((total, H, D), dtype=dtype, device=cache[0].device)
+    if k is None and v is None:
+        return None, None
+    st, pc, pl, pt, pk, pv, *codes = _on_current(cu, lens, table, k, v, *cache)
     st = _load().fp8sm_kv_cache_read(*codes, P, H, D, block, total, B, pc, pl, pt, ld_table, n,
-                                     _dtype_code(k), pk, ld_k, pv, ld_v, st)
+                                     _dtype_code(v if k is None else k), pk, ld_k, pv, ld_v, st)
     _check(st, "fp8sm_kv_cache_read")
     return k, v
 

@@ -49,3 +49,17 @@ def test_an_empty_batch_has_no_longest_sequence(kw):
     assert _attn(lib, mq=0, mkv=0, **kw) == E["OK"]
     assert _attn(lib, mq=-1, **kw) == _attn(lib, mkv=-1, **kw) == E["ERR_SHAPE"]
     assert _attn(lib, mq=0) == E["ERR_SHAPE"]
+
+
+def test_an_output_that_is_not_wanted_is_refused():
+    import torch
+    from column_scaled_gemm_amd import fp8sm
+    c = fp8sm.kv_cache_empty(3, 2, 64, 16, device="cpu")
+    i32 = dict(dtype=torch.int32)
+    rows = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    args = (c, torch.zeros(3, **i32), torch.zeros(2, **i32), torch.zeros(2, 4, **i32), 5)
+    for kw in (dict(k=rows, keys=False), dict(v=rows, values=False)):
+        with pytest.raises(ValueError):
+            fp8sm.kv_cache_read(*args, **kw)
+    with pytest.raises(fp8sm.DeviceTensorError):
+        fp8sm.kv_cache_read(*args, keys=False)

@@ -221,3 +221,21 @@ def test_empty_batches(T, B):
     got = fp8sm.kv_cache_read(c, cu, lens, table, T, k=torch.full_like(k, 5.0), v=torch.full_like(k, 5.0))
     for t, v in [(t, 7) for t in c] + [(t, 5) for t in (out, lse, *got)]:
         assert bool(torch.all(t == v))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_reading_keys_or_values_alone(dtype):
+    r = rng(71)
+    cu, L, table, blocks = batch(r, [3, 20], [40, 33], 16)
+    cache, d = dev_cache(random_cache(r, blocks, 2, 16, 64)), to_dev(cu, L, table)
+    k, v = fp8sm.kv_cache_read(cache, *d, 23, dtype=dtype)
+    k1, none = fp8sm.kv_cache_read(cache, *d, 23, dtype=dtype, values=False)
+    assert none is None and torch.equal(k1, k)
+    none, v1 = fp8sm.kv_cache_read(cache, *d, 23, dtype=dtype, keys=False)
+    assert none is None and torch.equal(v1, v)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    none, v2 = fp8sm.kv_cache_read(cache, *d, 23, dtype=dtype, keys=False, v=torch.zeros_like(v), stream=side)
+    side.synchronize()
+    assert none is None and torch.equal(v2, v)
+    assert fp8sm.kv_cache_read(cache, *d, 23, keys=False, values=False) == (None, None)
