@@ -239,3 +239,30 @@ def test_reading_keys_or_values_alone(dtype):
     side.synchronize()
     assert none is None and torch.equal(v2, v)
     assert fp8sm.kv_cache_read(cache, *d, 23, keys=False, values=False) == (None, None)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("kind", ["plain", "window", "full", "wide", "missing"])
+def test_long_walks_of_one_workgroup(kind, dtype, D):
+    """More steps than one gather of blocks and scales brings, thrice, unsplit: the
+    hint says one token."""
+    def damage(cu, L, table, ref):
+        if kind == "wide":
+            ref.exp[1][:] = rng(5).integers(100, 121, ref.exp[1].shape)
+        if kind == "missing":
+            table[0, 3], table[0, 200] = -1, ref.blocks
+
+    for n in ([70], [3]):       # the kernels for many and for few rows
+        run(n, [6500], 2, 1, D, 16, dtype, max_kv=1, window=5000 if kind == "window" else 0, causal=kind != "full",
+            damage=damage)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,lens", [([1, 3], [200, 65]), ([150, 2], [200, 65]), ([140, 80], [100, 0])])
+def test_without_causality_in_fp16(n, lens, D):
+    run(n, lens, 4, 2, D, 32, "fp16", causal=False)
+
+
+def test_long_contexts_without_causality_and_splits():
+    run([1, 90], [9000, 3000], 4, 2, 64, 64, "fp16", causal=False)
