@@ -66,8 +66,8 @@ def _join(parts, obj):
     if len(parts) == 1:
         shutil.copy(parts[0], obj)
         return
-    r = subprocess.run([shutil.which("ld") or "ld", "-r", "-o", obj] + parts,
-                       capture_output=True, text=True)
+    r = subprocess.run([_hipcc(), "-r", "-nostdlib", "-o", obj] + parts, capture_output=True,
+                       text=True)
     if r.returncode != 0:
         raise RuntimeError(f"joining {obj} failed:\n" + r.stdout + r.stderr)
 
