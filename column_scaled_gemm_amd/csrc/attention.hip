@@ -137,8 +137,8 @@ __device__ __forceinline__ float quarter_max(float v) {
 // Bound by the stream of codes from memory; every code goes straight from
 // memory to the registers of the lane that multiplies it, widened there.  A chip
 // full of such workgroups streams 5.3 .. 5.9 TB/s (64 sequences of 500 .. 16384
-// tokens, 8 key heads of 128, 1.13 GB: 195 .. 202 us with the join; two of
-// 131072 tokens with 32 rows, 0.54 GB: 95 .. 101 us), above the 4.9 TB/s at
+// tokens, 8 key heads of 128, 1.13 GB: 195 .. 203 us with the join; two of
+// 131072 tokens with 32 rows, 0.54 GB: 96 .. 105 us), above the 4.9 TB/s at
 // which a large copy reads and writes.
 // P is the sum of two bf16 values (2^-16 of p), so that V's widened codes stay exact in
 // bf16 whatever their blocks' scales and the results are those of an fp32 softmax but
@@ -483,10 +483,10 @@ __global__ __launch_bounds__(256, 2) void attn_few_kernel(AttnArgs a) {
 // (keys and values, 2 KB each at D = 128) straight into an LDS ring of three
 // steps; a run lies in one block, so its address is wavefront-uniform.  Block
 // numbers and scales are gathered 128 runs at a time into LDS.
-// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 1010 .. 1075 us, 0.92 .. 0.98
+// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 1020 .. 1080 us, 0.92 .. 0.97
 // PFLOP/s, where a bf16 library product of 16384^3 reaches 1.36.  Bound by vector
-// arithmetic (63% busy: widening 128 of a step's 300 instructions, the rest
-// softmax), the matrix instructions beside it (44%) and the clock, which real data
+// arithmetic (61% busy: widening 128 of a step's 300 instructions, the rest
+// softmax), the matrix instructions beside it (43%) and the clock, which real data
 // lowers by a fifth (920 us with constant operands).  Slower, measured: widening
 // once per workgroup through LDS (1093 against 1033 us); eight wavefronts in
 // alternating phases held apart by barriers (1273); the next step's scores
