@@ -414,6 +414,8 @@ fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
  * sees nothing gets zeros and lse -inf.  Statistics and sums are fp32; the
  * probabilities are rounded for the product with V, by at most half a step of
  * fp16 (2^-11 of each), or by 2^-32 of the row's largest where that is more.
+ * Scores and sums of probabilities times values beyond fp32's range (the latter
+ * with values above about 1e38 / the row's tokens) come out infinite or NaN.
  *   q, o  device bf16/fp16 [T][ld]: Hq heads of D values, 16-byte aligned, ld
  *         multiples of 8.  Hq a multiple of Hkv.
  *   lse   device fp32 [T][Hq] or NULL: ln of the sum of exp(scores).

@@ -266,3 +266,43 @@ def test_without_causality_in_fp16(n, lens, D):
 
 def test_long_contexts_without_causality_and_splits():
     run([1, 90], [9000, 3000], 4, 2, 64, 64, "fp16", causal=False)
+
+
+def test_a_mixed_batch_captured_and_replayed_with_other_rows_and_lengths():
+    """Both kernels, splits and the join; rows before, behind and of no sequence."""
+    r = rng(80)
+    H, D, block, T = 2, 64, 32, 130
+    cu0, L0, table, blocks = batch(r, [60, 1, 5], [5000, 5000, 5000], block)
+    cache = dev_cache(random_cache(r, blocks, H, block, D))
+    cu, lens, tab = to_dev(cu0, L0, table)
+    q = rows(r, T, 4, D).cuda()
+    x = rows(r, T, H, D).cuda()
+    out = torch.zeros_like(q)
+    lse = torch.zeros(T, 4, device="cuda")
+
+    def step(cache, out, lse):
+        fp8sm.kv_cache_write(x, x, cache, cu, lens, tab)
+        fp8sm.attention_cache(q, cache, cu, lens, tab, 100, max_kv=5000, out=out, lse=lse)
+
+    step(cache, out, lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(cache, out, lse)
+    for c, n in (([0, 60, 61, 66], [5000, 4000, 70]), ([30, 30, 130, 130], [9, 2600, 1]), ([0, 1, 2, 3], [4999, 17, 0]),
+                 ([100, 101, 110, 110], [5000, 9, 5000]), ([0, 60, 61, 66], [5000, 4000, 70])):
+        cu.copy_(torch.tensor(c, dtype=torch.int32))
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        mine = fp8sm.KVCache(*(t.clone() for t in cache))
+        want, want_l = torch.full_like(out, 5.0), torch.full_like(lse, 5.0)
+        step(mine, want, want_l)
+        out.fill_(5.0)
+        lse.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_l)
+        rest = torch.ones(T, dtype=torch.bool)
+        rest[c[0]:c[-1]] = False
+        assert torch.all(out.cpu()[rest] == 5) and torch.all(lse.cpu()[rest] == 5)
+        for a, b in zip(cache, mine):
+            assert torch.equal(a, b)
