@@ -18,8 +18,8 @@ LIB = os.path.join(HERE, "libfp8sm.so")
 # object -> sources; a family of kernels in several sources is one relocatable
 # object, so whoever links the host part anew names the same few objects
 OBJECTS = {
-    "quant.o": ["quant.hip", "kv_cache.hip"],
-    "gemm.o": ["gemm.hip", "attention.hip"],
+    "quant.o": ["quant.hip", "quant_int8.hip", "kv_cache.hip"],
+    "gemm.o": ["gemm.hip", "gemm_int8.hip", "attention.hip"],
     "probe.o": ["probe.hip"],
     "api.o": ["api.cpp"],
 }

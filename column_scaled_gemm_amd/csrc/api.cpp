@@ -53,9 +53,13 @@ constexpr int64_t kMaxK = 65536;
 // GEMM operand row strides (bytes): the kernels address up to 64 rows of A or
 // B with 32-bit offsets from one base, so 64 * stride + K must stay below 2^31.
 constexpr int64_t kMaxGemmLd = (int64_t)1 << 24;
+// Outputs of a batch of the int8 GEMM: a launch holds less than 2^32 threads.
+constexpr int64_t kMaxOutputs = (int64_t)1 << 37;
 constexpr int64_t kMaxTokens = (int64_t)1 << 23;
 constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
 constexpr int32_t kMaxHeads = 1024;
+// Rows of a batch of the int8 quant: one workgroup of 256 threads each, fewer than 2^32 a launch.
+constexpr int64_t kMaxQuantRows = ((int64_t)1 << 24) - 1;
 constexpr int64_t kMaxBatch = 65535;  // one grid row (blockIdx.y) per batch
 
 // Batch arguments common to every batched call: the count, non-negative
@@ -346,24 +350,28 @@ int fp8sm_pick_variant(int64_t M, int64_t N, int64_t K) {
   return pick_from_table(M, N, K);
 }
 
+// The kernels behind one set of argument checks.
+enum MmKernel { MM_FP8, MM_FP8MFMA, MM_INT8 };
+
 static fp8sm_status scaled_mm_impl(const uint8_t* A, int64_t lda, const uint8_t* B, int64_t ldb,
                                    void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
                                    fp8sm_scale_kind ka, const void* sa, fp8sm_scale_kind kb,
                                    const void* sb, const void* bias, fp8sm_dtype out,
                                    hipStream_t stream,
                                    const GemmBatch& bt = GemmBatch{1, 0, 0, 0, 0, 0, nullptr},
-                                   bool fp8mfma = false) {
+                                   MmKernel kernel = MM_FP8) {
   fp8sm_status bst = check_batch(bt.count, bt.rows, {bt.a, bt.b, bt.c, bt.sa, bt.sb});
   if (bst != FP8SM_OK) return bst;
   const bool rowwise = (ka == FP8SM_KIND_TENSOR || ka == FP8SM_KIND_ROW) &&
                        (kb == FP8SM_KIND_TENSOR || kb == FP8SM_KIND_COL);
   const bool blockwise = (ka == FP8SM_KIND_GROUP128_UE8M0 || ka == FP8SM_KIND_GROUP128_FP32) &&
                          kb == FP8SM_KIND_BLOCK128;
-  if (!rowwise && !blockwise) return FP8SM_ERR_UNSUPPORTED;
+  if (!rowwise && (!blockwise || kernel != MM_FP8)) return FP8SM_ERR_UNSUPPORTED;
   if (out != FP8SM_BF16 && out != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
   if (blockwise && (bias || out != FP8SM_BF16)) return FP8SM_ERR_UNSUPPORTED;
   if (M < 0 || N < 0 || K < 0) return FP8SM_ERR_SHAPE;
   if (M > kMaxDim || N > kMaxDim || K > kMaxK) return FP8SM_ERR_RANGE;
+  if (kernel == MM_INT8 && M * N > kMaxOutputs) return FP8SM_ERR_RANGE;
   if (lda < K || ldb < K || ldc < N) return FP8SM_ERR_SHAPE;
   if (lda > kMaxGemmLd || ldb > kMaxGemmLd) return FP8SM_ERR_RANGE;
   if (K % 16 || lda % 16 || ldb % 16 || bt.a % 16 || bt.b % 16) return FP8SM_ERR_ALIGN;
@@ -400,7 +408,8 @@ static fp8sm_status scaled_mm_impl(const uint8_t* A, int64_t lda, const uint8_t*
   g.bias = bias;
   g.out_f16 = out == FP8SM_FP16;
   g.batch = bt;
-  if (fp8mfma) return launched(launch_gemm_rowwise_fp8mfma(g, stream));
+  if (kernel == MM_FP8MFMA) return launched(launch_gemm_rowwise_fp8mfma(g, stream));
+  if (kernel == MM_INT8) return launched(launch_gemm_int8(g, stream));
   if (blockwise) return launched(launch_gemm_blockwise(g, stream));
   int v = fp8sm_pick_variant(M, N, K);
   if (!variant_accepts(v, M)) return FP8SM_ERR_UNSUPPORTED;
@@ -427,11 +436,8 @@ fp8sm_status fp8sm_scaled_mm_fp8mfma(const uint8_t* A, int64_t lda, const uint8_
                                      int64_t ldb, void* C, int64_t ldc, int64_t M, int64_t N,
                                      int64_t K, fp8sm_scale_kind ka, const void* sa,
                                      fp8sm_scale_kind kb, const void* sb, hipStream_t stream) {
-  const bool rowwise = (ka == FP8SM_KIND_TENSOR || ka == FP8SM_KIND_ROW) &&
-                       (kb == FP8SM_KIND_TENSOR || kb == FP8SM_KIND_COL);
-  if (!rowwise) return FP8SM_ERR_UNSUPPORTED;
   return scaled_mm_impl(A, lda, B, ldb, C, ldc, M, N, K, ka, sa, kb, sb, nullptr, FP8SM_BF16,
-                        stream, GemmBatch{1, 0, 0, 0, 0, 0, nullptr}, true);
+                        stream, GemmBatch{1, 0, 0, 0, 0, 0, nullptr}, MM_FP8MFMA);
 }
 
 fp8sm_status fp8sm_mfma_probe(int32_t instr, const uint32_t* a_regs, const uint32_t* b_regs,
@@ -467,6 +473,43 @@ fp8sm_status fp8sm_scaled_mm_batched(int64_t nbatch, const int32_t* rows, const 
                                      hipStream_t stream) {
   return scaled_mm_impl(A, lda, B, ldb, C, ldc, M, N, K, ka, sa, kb, sb, bias, out, stream,
                         GemmBatch{nbatch, bs_a, bs_b, bs_c, bs_sa, bs_sb, rows});
+}
+
+fp8sm_status fp8sm_scaled_mm_int8(int64_t nbatch, const int32_t* rows, const int8_t* A,
+                                  int64_t bs_a, int64_t lda, const int8_t* B, int64_t bs_b,
+                                  int64_t ldb, void* C, int64_t bs_c, int64_t ldc, int64_t M,
+                                  int64_t N, int64_t K, fp8sm_scale_kind ka, const float* sa,
+                                  int64_t bs_sa, fp8sm_scale_kind kb, const float* sb,
+                                  int64_t bs_sb, const void* bias, fp8sm_dtype out,
+                                  hipStream_t stream) {
+  return scaled_mm_impl(reinterpret_cast<const uint8_t*>(A), lda, reinterpret_cast<const uint8_t*>(B),
+                        ldb, C, ldc, M, N, K, ka, sa, kb, sb, bias, out, stream,
+                        GemmBatch{nbatch, bs_a, bs_b, bs_c, bs_sa, bs_sb, rows}, MM_INT8);
+}
+
+fp8sm_status fp8sm_quant_int8(const void* x, fp8sm_dtype in, int64_t nbatch, int64_t M,
+                              int64_t K_out, int64_t bs_x, int64_t ld_x, const int32_t* rows,
+                              uint32_t flags, int8_t* q, int64_t bs_q, int64_t ld_q,
+                              float* scales, hipStream_t stream) {
+  fp8sm_status st = check_batch(nbatch, rows, {bs_x, bs_q});
+  if (st != FP8SM_OK) return st;
+  if (in != FP8SM_BF16 && in != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
+  if (flags & ~FP8SM_FUSE_SILU_MUL) return FP8SM_ERR_UNSUPPORTED;
+  const bool fused = (flags & FP8SM_FUSE_SILU_MUL) != 0;
+  if (M < 0 || K_out <= 0) return FP8SM_ERR_SHAPE;
+  if (M > kMaxQuantRows || K_out > kMaxDim) return FP8SM_ERR_RANGE;
+  if (ld_x < (fused ? 2 * K_out : K_out) || ld_q < K_out) return FP8SM_ERR_SHAPE;
+  if (K_out % 8 || ld_x % 8 || ld_q % 8 || bs_x % 8 || bs_q % 8) return FP8SM_ERR_ALIGN;
+  if (!disjoint(nbatch, bs_q, M, ld_q, K_out)) return FP8SM_ERR_SHAPE;
+  if (M == 0 || nbatch == 0) return FP8SM_OK;
+  if (!x || !q || !scales) return FP8SM_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(q, 8) || !aligned(scales, 4)) return FP8SM_ERR_ALIGN;
+  st = check_device();
+  if (st != FP8SM_OK) return st;
+  return launched(launch_quant_int8(
+      QuantInt8Args{x, in == FP8SM_FP16, fused, M, K_out, ld_x, q, ld_q, scales,
+                    QuantBatch{nbatch, bs_x, bs_q, M, rows}},
+      stream));
 }
 
 // ---- QKV projection to attention

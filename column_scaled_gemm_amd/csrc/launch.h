@@ -45,6 +45,17 @@ struct QuantArgs {
 
 hipError_t launch_quant_group(const QuantArgs& a, hipStream_t s);
 
+struct QuantInt8Args {
+  const void* x;
+  bool f16, fused;
+  int64_t M, K, ld_x;
+  int8_t* q;
+  int64_t ld_q;
+  float* scales;  // [count][M]
+  QuantBatch batch;
+};
+hipError_t launch_quant_int8(const QuantInt8Args& a, hipStream_t s);
+
 struct ScatterArgs {
   const void* x;
   bool f16;
@@ -116,6 +127,8 @@ hipError_t launch_gemm_rowwise(int variant, const GemmArgs& g, hipStream_t s);
 hipError_t launch_gemm_blockwise(const GemmArgs& g, hipStream_t s);
 // The rowwise GEMM on the fp8 matrix instructions (evidence only: inexact).
 hipError_t launch_gemm_rowwise_fp8mfma(const GemmArgs& g, hipStream_t s);
+// int8 codes in A and B, rowwise / per-tensor scales.
+hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s);
 // One matrix instruction on host-supplied register images (probe.hip).
 hipError_t launch_mfma_probe(int instr, const uint32_t* a, const uint32_t* b, float* d,
                              hipStream_t s);

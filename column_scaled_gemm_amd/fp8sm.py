@@ -50,6 +50,10 @@ SIGNATURES = {
     "fp8sm_scaled_mm_batched": (_int, [_i64, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64,
                                        _i64, _i64, _i64, _int, _p, _i64, _int, _p, _i64, _p, _int,
                                        _p]),
+    "fp8sm_quant_int8": (_int, [_p, _int, _i64, _i64, _i64, _i64, _i64, _p, _u32, _p, _i64, _i64, _p,
+                                _p]),
+    "fp8sm_scaled_mm_int8": (_int, [_i64, _p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64,
+                                    _i64, _i64, _int, _p, _i64, _int, _p, _i64, _p, _int, _p]),
     "fp8sm_qk_norm_rope": (_int, [_p, _int, _i64, _i32, _i32, _i32, _i64, _p, _p, ctypes.c_float, _p,
                                   _i64, _p, _i32, _u32, _p, _i64, _p]),
     "fp8sm_kv_cache_write": (_int, [_p, _i64, _p, _i64, _int, _i64, _i64, _p, _p, _p, _i64, _i64,
@@ -571,6 +575,92 @@ def scaled_mm_batched(a, b, sa, sb, kind_a, kind_b, rows=None, c=None, bias=None
         _ptr(c), _bs(c, B), _ld(c), M, N, K, kind_a, _ptr(sa), bs_sa, kind_b,
         _ptr(sb), bs_sb, None if bias is None else _ptr(bias), out, _stream(stream))
     _check(st, "fp8sm_scaled_mm_batched")
+    return c
+
+
+# ---------------------------------------------------------------- 8-bit integers
+
+def _batched(t, what):
+    """(batches, rows, columns, batch stride, row stride) of a matrix or a batch of them."""
+    _unit_last(t, what)
+    if t.dim() == 2:
+        return 1, t.shape[0], t.shape[1], 0, _ld(t)
+    if t.dim() != 3:
+        raise ValueError(f"{what}: needs 2 or 3 dimensions, got {tuple(t.shape)}")
+    B, M, K = t.shape
+    return B, M, K, _bs(t, B), _ld(t)
+
+
+def quant_int8(x, fuse_silu_mul=False, rows=None, q=None, scales=None, stream=None):
+    """x [M, K_in] or [B, M, K_in] bf16/fp16 (K_in = 2*K_out when fused; any batch /
+    row strides) -> (codes int8 [.., M, K_out], scales fp32 [.., M]): per-token
+    symmetric quant, the operands of scaled_mm_int8.  rows: optional device int32
+    [B] live-row counts; the outputs of other rows are left as they were."""
+    if stream is not None:  # what is allocated here belongs to that stream then
+        with torch.cuda.stream(stream):
+            return quant_int8(x, fuse_silu_mul, rows, q, scales)
+    B, M, K_in, bs_x, ld_x = _batched(x, "x")
+    K = K_in // 2 if fuse_silu_mul else K_in
+    if fuse_silu_mul and K_in % 2:
+        raise ValueError("x: fuse_silu_mul needs [gate | up], an even number of columns")
+    lead = x.shape[:-1]
+    if q is None:
+        q = torch.empty(lead + (K,), dtype=torch.int8, device=x.device)
+    else:
+        _holds(q, lead + (K,), "q", torch.int8)
+    _, _, _, bs_q, ld_q = _batched(q, "q")
+    if scales is None:
+        scales = torch.empty(lead, dtype=torch.float32, device=x.device)
+    else:
+        _holds_bytes(scales, 4 * B * M, "scales", torch.float32)
+    rows = _rows_arg(rows, B)
+    st, px, pr, pq, ps = _on_current(x, rows, q, scales)
+    st = _load().fp8sm_quant_int8(px, _dtype_code(x), B, M, K, bs_x, ld_x, pr,
+                                  FUSE_SILU_MUL if fuse_silu_mul else 0, pq, bs_q, ld_q, ps, st)
+    _check(st, "fp8sm_quant_int8")
+    return q, scales
+
+
+def scaled_mm_int8(a, b, sa, sb, kind_a=KIND_ROW, kind_b=KIND_COL, rows=None, c=None, bias=None,
+                   out_dtype=None, stream=None):
+    """a [M, K] or [B, M, K] int8, b [N, K] (one weight) or [B, N, K] (one per
+    batch) int8 -> c [.., M, N] bf16, or fp16 with out_dtype=torch.float16: the int32
+    sums times sa (fp32 per row, or one scalar: KIND_TENSOR) and sb (per column, or a
+    scalar), each shared or with a leading batch dimension, plus bias [N] of the
+    output dtype.  rows: optional device int32 [B] live-row counts; rows past a
+    batch's count are left as c held them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return scaled_mm_int8(a, b, sa, sb, kind_a, kind_b, rows, c, bias, out_dtype)
+    if a.dtype != torch.int8 or b.dtype != torch.int8:
+        raise TypeError("a and b must be int8")
+    B, M, K, bs_a, lda = _batched(a, "a")
+    Bb, N, Kb, bs_b, ldb = _batched(b, "b")
+    if Kb != K or (b.dim() == 3 and (a.dim() == 2 or Bb != B)):
+        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} do not go together")
+    if out_dtype is None:
+        out_dtype = c.dtype if c is not None else torch.bfloat16
+    out = {torch.bfloat16: BF16, torch.float16: FP16}[out_dtype]
+    if c is None:
+        c = torch.empty(a.shape[:-1] + (N,), dtype=out_dtype, device=a.device)
+    else:
+        _holds(c, a.shape[:-1] + (N,), "c")
+    _, _, _, bs_c, ldc = _batched(c, "c")
+    if c.dtype != out_dtype or (bias is not None and bias.dtype != out_dtype):
+        raise TypeError("c and bias must have the output dtype")
+    if bias is not None:
+        _holds_bytes(bias, 2 * N, "bias")
+    if kind_a not in (KIND_TENSOR, KIND_ROW) or kind_b not in (KIND_TENSOR, KIND_COL):
+        raise ValueError("scale kinds: TENSOR or ROW for a, TENSOR or COL for b")
+    if sa.dtype != torch.float32 or sb.dtype != torch.float32:
+        raise TypeError("sa and sb must be float32")
+    bs_sa = _scale_batch_stride(sa, kind_a, B, 1 if kind_a == KIND_TENSOR else M, "sa")
+    bs_sb = _scale_batch_stride(sb, kind_b, B, 1 if kind_b == KIND_TENSOR else N, "sb")
+    rows = _rows_arg(rows, B)
+    st, pa, pr, pb, pc, psa, psb, pbias = _on_current(a, rows, b, c, sa, sb, bias)
+    st = _load().fp8sm_scaled_mm_int8(B, pr, pa, bs_a, lda, pb, bs_b, ldb, pc, bs_c, ldc, M, N, K,
+                                      kind_a, psa, bs_sa, kind_b, psb, bs_sb, pbias, out, st)
+    _check(st, "fp8sm_scaled_mm_int8")
     return c
 
 

@@ -266,6 +266,45 @@ fp8sm_status fp8sm_scaled_mm_batched(int64_t nbatch, const int32_t* rows, const 
                                      hipStream_t stream);
 
 /*
+ * ---- 8-bit integers ----
+ *
+ * Per-token int8 quant, the counterpart of fp8sm_quant_group for fp8sm_scaled_mm_int8.
+ * For each row of K_out values y, in fp32:
+ *   a' = max(max|y|, 1e-10);  scale = RN32(a' / 127);  q = RNE(RN32(y * RN32(127 / a')))
+ * rounded to the nearest integer, ties to even, so -127 <= q <= 127.  Infinities and
+ * NaN take no part in a'; an infinity becomes +-127, a NaN 0.
+ *   x, in, M, K_out, ld_x, flags  as fp8sm_quant_group: with FP8SM_FUSE_SILU_MUL a row
+ *          is [gate | up] and y = RN32(silu(gate) * up) with the same silu (a NaN gate,
+ *          or -inf, gives a NaN y).
+ *   nbatch, bs_x, bs_q, rows  as in the batched forms above (1, 0, 0, NULL: one matrix).
+ *   q      device int8 [nbatch][M][ld_q].  scales: device fp32 [nbatch][M].
+ * Errors as fp8sm_quant_group_batched; M >= 2^24 -> ERR_RANGE.
+ */
+fp8sm_status fp8sm_quant_int8(const void* x, fp8sm_dtype in, int64_t nbatch, int64_t M,
+                              int64_t K_out, int64_t bs_x, int64_t ld_x, const int32_t* rows,
+                              uint32_t flags, int8_t* q, int64_t bs_q, int64_t ld_q,
+                              float* scales, hipStream_t stream);
+
+/*
+ * Scaled int8 GEMM with an optional bias:
+ *   C[m,n] = rnd( RN32( RN32(RN32(acc[m,n]) * sa[m]) * sb[n] ) + bias[n] )
+ * acc = sum_k A[m,k] * B[n,k], exact in int32 (all codes, -128 included).  Row m of C
+ * depends only on row m of A, B, the scales and the bias.
+ *   A, B   device int8 [M][lda], [N][ldb], K contiguous.
+ * Everything else -- scale kinds {TENSOR, ROW} x {TENSOR, COL}, bias, output type,
+ * alignment rules, K == 0, batches, strides in elements, live rows, errors -- is as for
+ * fp8sm_scaled_mm_batched (nbatch 1, strides 0, rows NULL: one product); a product of
+ * more than 2^37 outputs is ERR_RANGE.
+ */
+fp8sm_status fp8sm_scaled_mm_int8(int64_t nbatch, const int32_t* rows, const int8_t* A,
+                                  int64_t bs_a, int64_t lda, const int8_t* B, int64_t bs_b,
+                                  int64_t ldb, void* C, int64_t bs_c, int64_t ldc, int64_t M,
+                                  int64_t N, int64_t K, fp8sm_scale_kind ka, const float* sa,
+                                  int64_t bs_sa, fp8sm_scale_kind kb, const float* sb,
+                                  int64_t bs_sb, const void* bias, fp8sm_dtype out,
+                                  hipStream_t stream);
+
+/*
  * Load-time preparation of a fused per-tensor weight ([P3] key source
  * excerpts: the weights-after-loading step requantizes the fused weight to
  * its largest partition scale, then broadcasts scalar scales per channel when
