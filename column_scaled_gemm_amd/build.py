@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libfp8sm.so")
 # object, so whoever links the host part anew names the same few objects
 OBJECTS = {
     "quant.o": ["quant.hip", "quant_int8.hip", "kv_cache.hip"],
-    "gemm.o": ["gemm.hip", "gemm_int8.hip", "attention.hip"],
+    "gemm.o": ["gemm.hip", "gemm_int8.hip", "attention.hip", "attention_packed.hip"],
     "probe.o": ["probe.hip"],
     "api.o": ["api.cpp"],
 }

@@ -56,6 +56,8 @@ constexpr int64_t kMaxGemmLd = (int64_t)1 << 24;
 // Outputs of a batch of the int8 GEMM: a launch holds less than 2^32 threads.
 constexpr int64_t kMaxOutputs = (int64_t)1 << 37;
 constexpr int64_t kMaxTokens = (int64_t)1 << 23;
+// Row strides of packed keys and values (elements): a step's 64 rows have 32-bit offsets.
+constexpr int64_t kMaxKvLd = (int64_t)1 << 23;
 constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
 constexpr int32_t kMaxHeads = 1024;
 // Rows of a batch of the int8 quant: one workgroup of 256 threads each, fewer than 2^32 a launch.
@@ -545,11 +547,18 @@ static fp8sm_status kv_args(int64_t T, int64_t nseq, const int32_t* cu, const in
   return FP8SM_OK;
 }
 
-fp8sm_status fp8sm_qk_norm_rope(const void* x, fp8sm_dtype in, int64_t T, int32_t Hq, int32_t Hk,
-                                int32_t D, int64_t ld_x, const void* q_weight,
-                                const void* k_weight, float eps, const float* cos_sin,
-                                int64_t max_pos, const int32_t* pos, int32_t rot, uint32_t flags,
-                                void* y, int64_t ld_y, hipStream_t stream) {
+// Positions on several axes: their row stride, and two bits for each pair's axis.
+struct RopeAxes {
+  int n;
+  int64_t ld_pos;
+  uint64_t of[2];
+};
+
+static fp8sm_status rope_impl(const void* x, fp8sm_dtype in, int64_t T, int32_t Hq, int32_t Hk,
+                              int32_t D, int64_t ld_x, const void* q_weight, const void* k_weight,
+                              float eps, const float* cos_sin, int64_t max_pos, const int32_t* pos,
+                              int32_t rot, uint32_t flags, void* y, int64_t ld_y,
+                              hipStream_t stream, const RopeAxes* axes) {
   if (in != FP8SM_BF16 && in != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
   if (flags & ~FP8SM_ROPE_INTERLEAVED) return FP8SM_ERR_UNSUPPORTED;
   if (D != 64 && D != 128) return FP8SM_ERR_UNSUPPORTED;
@@ -587,7 +596,41 @@ fp8sm_status fp8sm_qk_norm_rope(const void* x, fp8sm_dtype in, int64_t T, int32_
   a.interleaved = (flags & FP8SM_ROPE_INTERLEAVED) != 0;
   a.y = y;
   a.ld_y = ld_y;
+  if (axes && rot > 0) {
+    a.axes = axes->n;
+    a.ld_pos = axes->ld_pos;
+    a.axis_of[0] = axes->of[0];
+    a.axis_of[1] = axes->of[1];
+  }
   return launched(launch_qk_norm_rope(a, stream));
+}
+
+fp8sm_status fp8sm_qk_norm_rope(const void* x, fp8sm_dtype in, int64_t T, int32_t Hq, int32_t Hk,
+                                int32_t D, int64_t ld_x, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos_sin,
+                                int64_t max_pos, const int32_t* pos, int32_t rot, uint32_t flags,
+                                void* y, int64_t ld_y, hipStream_t stream) {
+  return rope_impl(x, in, T, Hq, Hk, D, ld_x, q_weight, k_weight, eps, cos_sin, max_pos, pos, rot,
+                   flags, y, ld_y, stream, nullptr);
+}
+
+fp8sm_status fp8sm_qk_norm_rope_axes(const void* x, fp8sm_dtype in, int64_t T, int32_t Hq,
+                                     int32_t Hk, int32_t D, int64_t ld_x, const void* q_weight,
+                                     const void* k_weight, float eps, const float* cos_sin,
+                                     int64_t max_pos, const int32_t* pos, int64_t ld_pos,
+                                     int32_t naxes, const uint8_t* axes, int32_t rot,
+                                     uint32_t flags, void* y, int64_t ld_y, hipStream_t stream) {
+  if (naxes < 1 || rot < 0 || (ld_pos != 0 && ld_pos < T)) return FP8SM_ERR_SHAPE;
+  if (naxes > kMaxAxes) return FP8SM_ERR_RANGE;
+  if (rot > 128) return FP8SM_ERR_SHAPE;  // (beyond any D: `axes` is not read past 64)
+  RopeAxes r{naxes, ld_pos, {0, 0}};
+  if (rot > 0 && !axes) return FP8SM_ERR_NULL;
+  for (int i = 0; i < rot / 2; ++i) {
+    if (axes[i] >= naxes) return FP8SM_ERR_SHAPE;
+    r.of[i / 32] |= (uint64_t)axes[i] << (2 * (i % 32));
+  }
+  return rope_impl(x, in, T, Hq, Hk, D, ld_x, q_weight, k_weight, eps, cos_sin, max_pos, pos, rot,
+                   flags, y, ld_y, stream, &r);
 }
 
 fp8sm_status fp8sm_kv_cache_write(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
@@ -631,6 +674,12 @@ fp8sm_status fp8sm_kv_cache_read(const uint8_t* k_codes, const uint8_t* v_codes,
   st = check_device();
   if (st != FP8SM_OK) return st;
   return launched(launch_kv_read(kb, c, k, v, out == FP8SM_FP16, ld_k, ld_v, stream));
+}
+
+// The factor of scores as exponents of 2.  0 becomes the smallest normal one, so that a
+// masked -inf stays -inf; none is infinite, so that a score of 0 stays 0.
+static float score_factor(float scale) {
+  return std::min(std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN), FLT_MAX);
 }
 
 // Sizes that fp8sm_attention_cache's plan and workspace rest on.
@@ -687,9 +736,7 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   a.lse = lse;
   a.Hq = Hq;
   a.G = Hq / Hkv;
-  // 0 becomes the smallest normal factor, so that a masked -inf stays -inf; none
-  // is infinite, so that a score of 0 stays 0
-  a.scale_log2 = std::min(std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN), FLT_MAX);
+  a.scale_log2 = score_factor(scale);
   a.negate = scale < 0.f;
   a.causal = (flags & FP8SM_ATTN_CAUSAL) != 0;
   // no sequence is longer than kMaxDim: such a window bounds nothing (and a row's
@@ -705,6 +752,53 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
   a.few_by_seq = p.few_by_seq;
   a.row_limit = p.row_limit;
   return launched(launch_attention(a, in == FP8SM_FP16, p, stream));
+}
+
+fp8sm_status fp8sm_attention_packed(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                                    const void* v, int64_t ld_v, fp8sm_dtype in, int64_t T,
+                                    int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                                    const int32_t* cu, float scale, uint32_t flags, int32_t window,
+                                    void* o, int64_t ld_o, float* lse, hipStream_t stream) {
+  if (in != FP8SM_BF16 && in != FP8SM_FP16) return FP8SM_ERR_UNSUPPORTED;
+  if (flags & ~FP8SM_ATTN_CAUSAL) return FP8SM_ERR_UNSUPPORTED;
+  if (T < 0 || nseq < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || window < 0 || !std::isfinite(scale))
+    return FP8SM_ERR_SHAPE;
+  if (D != 64 && D != 128) return FP8SM_ERR_UNSUPPORTED;
+  if (window > 0 && !(flags & FP8SM_ATTN_CAUSAL)) return FP8SM_ERR_UNSUPPORTED;
+  if (T > kMaxTokens || nseq > kMaxSeqs || Hq > kMaxHeads || T * Hq > kMaxDim) return FP8SM_ERR_RANGE;
+  const int64_t row_q = (int64_t)Hq * D, row_k = (int64_t)Hkv * D;
+  if (ld_q < row_q || ld_o < row_q || ld_k < row_k || ld_v < row_k) return FP8SM_ERR_SHAPE;
+  if (ld_k > kMaxKvLd || ld_v > kMaxKvLd) return FP8SM_ERR_RANGE;
+  if (ld_q % 8 || ld_k % 8 || ld_v % 8 || ld_o % 8) return FP8SM_ERR_ALIGN;
+  if (T == 0 || nseq == 0) return FP8SM_OK;
+  if (!q || !k || !v || !cu || !o) return FP8SM_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(cu, 4) ||
+      !aligned(lse, 4))
+    return FP8SM_ERR_ALIGN;
+  const fp8sm_status st = check_device();
+  if (st != FP8SM_OK) return st;
+  PackedArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.ld_q = ld_q;
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.out = static_cast<uint16_t*>(o);
+  a.ld_o = ld_o;
+  a.lse = lse;
+  a.cu = cu;
+  a.T = (int)T;
+  a.B = (int)nseq;
+  a.Hq = Hq;
+  a.heads = Hkv;
+  a.G = Hq / Hkv;
+  a.D = D;
+  a.scale_log2 = score_factor(scale);
+  a.negate = scale < 0.f;
+  a.causal = (flags & FP8SM_ATTN_CAUSAL) != 0;
+  a.window = window >= kMaxDim ? 0 : window;
+  return launched(launch_attention_packed(a, in == FP8SM_FP16, stream));
 }
 
 }  // extern "C"

@@ -16,29 +16,12 @@
 // is how the product O^T = V^T P^T wants its second operand, and V's cache
 // layout holds consecutive tokens of one channel, which is its first: neither
 // P nor V is moved between lanes.
-#include "kv_common.h"
+#include "attn_common.h"
 
 #include <algorithm>
 #include <type_traits>
 
 namespace fp8sm {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-// The running maximum is moved only when a row's scores exceed it by more than
-// kSlack (p <= 2^kSlack then), so most steps do not rescale the accumulator.
-constexpr float kSlack = 8.0f;
-// Where P is rounded to fp16 it is taken 2^kLift times as large: p <= 2^(kSlack +
-// kLift) = 2^15, which fp16 holds, and its fixed step below 2^-14 lies at 2^-31 of the
-// row's largest p.  Without the lift it is 2^-24, and a tail 16 nats below a token of
-// small value is off by 6%, one of 18 nats lost.
-constexpr float kLift = 7.0f, kUnlift = 1.0f / 128;
-// Up to here m scale rounds by at most 2^-4 and serves as the exponents' reference in one
-// fma; beyond, scores are subtracted first.
-constexpr float kFarScore = 1 << 20;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // Eight codes widened times a power of two, exactly unless the result leaves
 // the type's range.
@@ -55,14 +38,6 @@ __device__ __forceinline__ f16x8 widen_f16(uint32_t d0, uint32_t d1, float s) {
   const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d1, s, false);
   const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(d1, s, true);
   return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-template <bool F16>
-__device__ __forceinline__ uint16_t round16(float v) {
-  if constexpr (F16)
-    return __builtin_bit_cast(uint16_t, (_Float16)v);
-  else
-    return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 // Byte mask of a dword whose bytes are tokens t .. t + 3: those in [lo, hi).
@@ -113,19 +88,7 @@ __device__ __forceinline__ int64_t part_row(const AttnArgs& a, bool few, int b, 
   return few && a.few_by_seq ? ((int64_t)b * kFewRows + r) * a.c.heads + head / a.G : t * a.Hq + head;
 }
 
-// Grids are one list of workgroups; more than a grid's first dimension takes
-// go on in its second.
-constexpr uint32_t kGridX = 1 << 16;
-__device__ __forceinline__ int64_t workgroup_id() { return blockIdx.x + (int64_t)blockIdx.y * kGridX; }
-static dim3 grid_of(int64_t n) {
-  return n <= kGridX ? dim3((uint32_t)n) : dim3(kGridX, (uint32_t)((n + kGridX - 1) / kGridX));
-}
-
-// max of a value over the two half-wavefronts, and over the four quarters
-__device__ __forceinline__ float half_max(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
+// max over the four quarters of a wavefront
 __device__ __forceinline__ float quarter_max(float v) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));

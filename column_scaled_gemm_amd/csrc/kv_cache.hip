@@ -58,7 +58,10 @@ __device__ __forceinline__ void store_stream16(void* p, const uint4 v) {
 
 constexpr int kRopeU = 4;  // (8320 rows of 112 heads: 1: 119 us, 2: 108, 4: 100)
 
-template <bool F16, int D, bool NORM, bool INTER>
+//
+// AXES: pair i turns by row pos[axis(i)][t].  The token's rot cosines and sines are
+// gathered into LDS once for the workgroup's heads.
+template <bool F16, int D, bool NORM, bool INTER, bool AXES>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
   constexpr int LPH = D / 8, HPW = 64 / LPH;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -68,10 +71,24 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + t * a.ld_x;
   uint16_t* y = static_cast<uint16_t*>(a.y) + t * a.ld_y;
   const int h0 = (blockIdx.y * 4 + w) * (HPW * kRopeU) + sub;
-  if (h0 - sub >= heads) return;
+  if (!AXES && h0 - sub >= heads) return;
 
   int64_t p = 0;
-  if (a.rot) {
+  float gathered = 0.f;
+  if constexpr (AXES) {
+    int pa[kMaxAxes];
+#pragma unroll
+    for (int k = 0; k < kMaxAxes; ++k) {
+      pa[k] = a.pos[min(k, a.axes - 1) * a.ld_pos + t];
+      if (pa[k] < 0 || pa[k] >= a.max_pos) return;  // (the whole workgroup)
+    }
+    if ((int)threadIdx.x < a.rot) {
+      const int i = threadIdx.x, pair = i < half ? i : i - half;
+      const int axis = (int)((pair < 32 ? a.axis_of[0] : a.axis_of[1]) >> (2 * (pair & 31))) & 3;
+      const int row = axis == 0 ? pa[0] : axis == 1 ? pa[1] : axis == 2 ? pa[2] : pa[3];
+      gathered = a.cos_sin[(int64_t)row * a.rot + i];
+    }
+  } else if (a.rot) {
     p = a.pos[t];
     if (p < 0 || p >= a.max_pos) return;  // names no row of the table: left as it is
   }
@@ -81,11 +98,17 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
     const int h = min(h0 + u * HPW, heads - 1);
     v[u] = load_stream16(x + (int64_t)h * D + lh * 8);
   }
+  __shared__ float turns[AXES ? D : 1];
+  if constexpr (AXES) {
+    if ((int)threadIdx.x < a.rot) turns[threadIdx.x] = gathered;
+    __syncthreads();
+    if (h0 - sub >= heads) return;
+  }
   // the lane's pairs: 8 lh + i with 8 lh + i +- half, or adjacent elements
   const bool turned = lh * 8 < a.rot, first = lh * 8 < half;
   float cs[8], sn[8];
   if (turned) {
-    const float* row = a.cos_sin + p * a.rot;
+    const float* row = AXES ? turns : a.cos_sin + p * a.rot;
     if constexpr (INTER) {
       const float4 c = *reinterpret_cast<const float4*>(row + lh * 4);
       const float4 s = *reinterpret_cast<const float4*>(row + half + lh * 4);
@@ -154,28 +177,33 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
   }
 }
 
-template <bool F16, int D>
+template <bool F16, int D, bool AXES>
 static void rope_launch(const RopeArgs& a, hipStream_t s) {
   constexpr int per = 4 * (64 / (D / 8)) * kRopeU;
   const dim3 grid((uint32_t)a.T, (uint32_t)((a.Hq + a.Hk + per - 1) / per));
   if (a.wq || a.wk) {
     if (a.interleaved)
-      qk_norm_rope_kernel<F16, D, true, true><<<grid, 256, 0, s>>>(a);
+      qk_norm_rope_kernel<F16, D, true, true, AXES><<<grid, 256, 0, s>>>(a);
     else
-      qk_norm_rope_kernel<F16, D, true, false><<<grid, 256, 0, s>>>(a);
+      qk_norm_rope_kernel<F16, D, true, false, AXES><<<grid, 256, 0, s>>>(a);
   } else {
     if (a.interleaved)
-      qk_norm_rope_kernel<F16, D, false, true><<<grid, 256, 0, s>>>(a);
+      qk_norm_rope_kernel<F16, D, false, true, AXES><<<grid, 256, 0, s>>>(a);
     else
-      qk_norm_rope_kernel<F16, D, false, false><<<grid, 256, 0, s>>>(a);
+      qk_norm_rope_kernel<F16, D, false, false, AXES><<<grid, 256, 0, s>>>(a);
   }
 }
 
-hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t s) {
+template <bool AXES>
+static void rope_launch_of(const RopeArgs& a, hipStream_t s) {
   if (a.D == 64)
-    a.f16 ? rope_launch<true, 64>(a, s) : rope_launch<false, 64>(a, s);
+    a.f16 ? rope_launch<true, 64, AXES>(a, s) : rope_launch<false, 64, AXES>(a, s);
   else
-    a.f16 ? rope_launch<true, 128>(a, s) : rope_launch<false, 128>(a, s);
+    a.f16 ? rope_launch<true, 128, AXES>(a, s) : rope_launch<false, 128, AXES>(a, s);
+}
+
+hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t s) {
+  a.axes ? rope_launch_of<true>(a, s) : rope_launch_of<false>(a, s);
   return hipGetLastError();
 }
 

@@ -156,6 +156,8 @@ struct KvCache {
   int num_blocks, heads, D, block_shift;
 };
 
+constexpr int kMaxAxes = 4;  // of positions
+
 struct RopeArgs {
   const void* x;
   bool f16;
@@ -171,6 +173,9 @@ struct RopeArgs {
   bool interleaved;
   void* y;
   int64_t ld_y;
+  int axes = 0;            // 0: one position a row; else pos is [axes][ld_pos]
+  int64_t ld_pos = 0;
+  uint64_t axis_of[2] = {0, 0};  // two bits a pair: its axis
 };
 hipError_t launch_qk_norm_rope(const RopeArgs& a, hipStream_t s);
 hipError_t launch_kv_write(const void* k, const void* v, bool f16, int64_t ld_k, int64_t ld_v,
@@ -223,5 +228,19 @@ struct AttnPlan {
 AttnPlan plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, int64_t max_q, int64_t max_kv,
                         int64_t window);
 hipError_t launch_attention(const AttnArgs& a, bool f16, const AttnPlan& p, hipStream_t s);
+
+// Packed prompts: rows cu[b] .. cu[b+1]-1 of the token arrays are prompt b's.
+struct PackedArgs {
+  const uint16_t *q, *k, *v;
+  int64_t ld_q, ld_k, ld_v;
+  uint16_t* out;
+  int64_t ld_o;
+  float* lse;  // [T][Hq] or nullptr
+  const int32_t* cu;
+  int T, B, Hq, heads, G, D;  // heads: of keys and values
+  float scale_log2;           // |softmax scale| * log2(e), above 0
+  int negate, causal, window;
+};
+hipError_t launch_attention_packed(const PackedArgs& a, bool f16, hipStream_t s);
 
 }  // namespace fp8sm

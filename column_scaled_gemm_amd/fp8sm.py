@@ -56,6 +56,11 @@ SIGNATURES = {
                                     _i64, _i64, _int, _p, _i64, _int, _p, _i64, _p, _int, _p]),
     "fp8sm_qk_norm_rope": (_int, [_p, _int, _i64, _i32, _i32, _i32, _i64, _p, _p, ctypes.c_float, _p,
                                   _i64, _p, _i32, _u32, _p, _i64, _p]),
+    "fp8sm_qk_norm_rope_axes": (_int, [_p, _int, _i64, _i32, _i32, _i32, _i64, _p, _p,
+                                       ctypes.c_float, _p, _i64, _p, _i64, _i32, ctypes.c_char_p, _i32,
+                                       _u32, _p, _i64, _p]),
+    "fp8sm_attention_packed": (_int, [_p, _i64, _p, _i64, _p, _i64, _int, _i64, _i64, _i32, _i32, _i32,
+                                      _p, ctypes.c_float, _u32, _i32, _p, _i64, _p, _p]),
     "fp8sm_kv_cache_write": (_int, [_p, _i64, _p, _i64, _int, _i64, _i64, _p, _p, _p, _i64, _i64,
                                     _i64, _i32, _i32, _i32, _p, _p, _p, _p, _p]),
     "fp8sm_kv_cache_read": (_int, [_p, _p, _p, _p, _i64, _i32, _i32, _i32, _i64, _i64, _p, _p, _p,
@@ -765,6 +770,23 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_
         with torch.cuda.stream(stream):
             return qk_norm_rope(x, q_heads, k_heads, head_dim, positions, cos_sin, q_weight,
                                 k_weight, eps, interleaved, out)
+    args, out = _rope_args(x, q_heads, k_heads, head_dim, cos_sin, q_weight, k_weight, out)
+    T, rot = x.shape[0], args[1]
+    if cos_sin is not None:
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+        _holds_bytes(positions, 4 * T, "positions", torch.int32)
+    st, px, pq, pk, pc, pp, po = _on_current(x, q_weight, k_weight, cos_sin, positions, out)
+    ld_x, ld_y = _rope_strides(x, out, T, px, po)
+    st = _load().fp8sm_qk_norm_rope(px, _dtype_code(x), T, q_heads, k_heads, head_dim, ld_x,
+                                    pq, pk, eps, pc, args[0], pp, rot,
+                                    ROPE_INTERLEAVED if interleaved else 0, po, ld_y, st)
+    _check(st, "fp8sm_qk_norm_rope")
+    return out
+
+
+def _rope_args(x, q_heads, k_heads, head_dim, cos_sin, q_weight, k_weight, out):
+    """((rows of the table, rot), out), after the checks that both rotations share."""
     T = x.shape[0]
     row = (q_heads + k_heads) * head_dim
     _unit_last(x, "x")
@@ -780,20 +802,61 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions=None, cos_sin=None, q_
             raise ValueError("cos_sin: needs [positions, rot]")
         max_pos, rot = cos_sin.shape
         _holds_bytes(cos_sin, 0, "cos_sin", torch.float32)
-        if positions is None:
-            raise ValueError("cos_sin needs positions")
-        _holds_bytes(positions, 4 * T, "positions", torch.int32)
     for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None:
             _holds_bytes(t, 2 * head_dim, what, x.dtype)
-    st, px, pq, pk, pc, pp, po = _on_current(x, q_weight, k_weight, cos_sin, positions, out)
+    return (max_pos, rot), out
+
+
+def _rope_strides(x, out, T, px, po):
     ld_x, ld_y = _row_ld(x), _row_ld(out)
     if T <= 1 and po == px:  # in place: one stride, also where none is used
         ld_x = ld_y = max(ld_x, ld_y)
-    st = _load().fp8sm_qk_norm_rope(px, _dtype_code(x), T, q_heads, k_heads, head_dim, ld_x,
-                                    pq, pk, eps, pc, max_pos, pp, rot,
-                                    ROPE_INTERLEAVED if interleaved else 0, po, ld_y, st)
-    _check(st, "fp8sm_qk_norm_rope")
+    return ld_x, ld_y
+
+
+def rope_axes(sections, mixed=False):
+    """The axis of each pair of a head, for qk_norm_rope_axes: sections[a] pairs of
+    axis a, one section behind the other, or with mixed=True in turn while they last
+    (0, 1, 2, 0, 1, 2, ..)."""
+    if not mixed:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, axes = list(sections), []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                axes.append(a)
+                left[a] -= 1
+    return axes
+
+
+def qk_norm_rope_axes(x, q_heads, k_heads, head_dim, positions, cos_sin, axes, q_weight=None,
+                      k_weight=None, eps=1e-6, interleaved=False, out=None, stream=None):
+    """qk_norm_rope with positions on 1 to 4 axes: positions device int32 [axes, T] (any
+    row stride), cos_sin device fp32 [positions, rot], axes: the axis of each of the
+    rot/2 pairs (host integers or bytes, e.g. of rope_axes).  Pair i of row t turns by
+    column i of the table's row positions[axes[i], t]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_norm_rope_axes(x, q_heads, k_heads, head_dim, positions, cos_sin, axes, q_weight,
+                                     k_weight, eps, interleaved, out)
+    (max_pos, rot), out = _rope_args(x, q_heads, k_heads, head_dim, cos_sin, q_weight, k_weight, out)
+    T = x.shape[0]
+    if positions.dim() != 2 or positions.shape[1] != T or (T > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions: needs [axes, {T}] with contiguous rows, got {tuple(positions.shape)}")
+    if positions.dtype != torch.int32:
+        raise TypeError("positions must be int32")
+    n = positions.shape[0]
+    if not isinstance(axes, bytes):
+        axes = bytes(axes)
+    if len(axes) != rot // 2:
+        raise ValueError(f"axes: needs the axis of each of {rot // 2} pairs, got {len(axes)}")
+    st, px, pq, pk, pc, pp, po = _on_current(x, q_weight, k_weight, cos_sin, positions, out)
+    ld_x, ld_y = _rope_strides(x, out, T, px, po)
+    st = _load().fp8sm_qk_norm_rope_axes(px, _dtype_code(x), T, q_heads, k_heads, head_dim, ld_x, pq, pk,
+                                         eps, pc, max_pos, pp, positions.stride(0) if n > 1 else T, n, axes,
+                                         rot, ROPE_INTERLEAVED if interleaved else 0, po, ld_y, st)
+    _check(st, "fp8sm_qk_norm_rope_axes")
     return out
 
 
@@ -959,4 +1022,44 @@ def attention_cache(q, cache, cu, lens, table, max_q, max_kv=None, scale=None, c
         max_kv, D ** -0.5 if scale is None else scale, ATTN_CAUSAL if causal else 0, window, po,
         ld_o, pe, pw, need, st)
     _check(st, "fp8sm_attention_cache")
+    return (out, lse) if return_lse else out
+
+
+def attention_packed(q, k, v, cu, scale=None, causal=True, window=0, out=None, lse=None,
+                     return_lse=False, stream=None):
+    """q [T, Hq, D], k and v [T, H, D] bf16/fp16 (any row strides, e.g. columns of one
+    projection): attention of packed prompts over their own keys and values, prompt
+    b's tokens being the rows cu[b] .. cu[b+1]-1 (device int32 [prompts + 1]) -> out
+    [T, Hq, D], or (out, lse fp32 [T, Hq]) with return_lse.  Hq is a multiple of H, D
+    64 or 128; scale defaults to D^-1/2; causal=False: every token sees its whole
+    prompt.  out=q works in place."""
+    if stream is not None:  # what is allocated here belongs to that stream then
+        with torch.cuda.stream(stream):
+            return attention_packed(q, k, v, cu, scale, causal, window, out, lse, return_lse)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k: need [T, heads, D]")
+    Hq, (_, H, D) = q.shape[1], k.shape
+    T, ld_q = _head_rows(q, Hq, D, "q")
+    Tk, ld_k = _head_rows(k, H, D, "k")
+    Tv, ld_v = _head_rows(v, H, D, "v")
+    if Tk != T or Tv != T or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have the same rows and dtype")
+    if cu.dtype != torch.int32:
+        raise TypeError("cu must be int32")
+    if cu.dim() != 1 or cu.numel() < 1 or not cu.is_contiguous():
+        raise ValueError("cu: needs [prompts + 1], contiguous")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        ld_o = Hq * D
+    else:
+        ld_o = _out_rows(out, T, Hq, D, q.dtype, "out")
+    if lse is not None:
+        _holds_bytes(lse, 4 * T * Hq, "lse", torch.float32)
+    elif return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    st, pq, pk, pv, pc, po, pe = _on_current(q, k, v, cu, out, lse)
+    st = _load().fp8sm_attention_packed(pq, ld_q, pk, ld_k, pv, ld_v, _dtype_code(q), T, cu.numel() - 1, Hq,
+                                        H, D, pc, D ** -0.5 if scale is None else scale,
+                                        ATTN_CAUSAL if causal else 0, _window(window), po, ld_o, pe, st)
+    _check(st, "fp8sm_attention_packed")
     return (out, lse) if return_lse else out

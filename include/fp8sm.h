@@ -408,6 +408,27 @@ fp8sm_status fp8sm_qk_norm_rope(const void* x, fp8sm_dtype in, int64_t T, int32_
                                 void* y, int64_t ld_y, hipStream_t stream);
 
 /*
+ * The same with positions on several axes (time, height, width of a picture's or a
+ * video's patches): pair i of a head, i < rot/2, turns by column i of the table's row
+ * pos[axes[i]][t].  A text token has the same position on every axis; axes with
+ * frequencies of their own have them in their columns of the table.
+ *   naxes  1..4.  axes: HOST uint8 [rot/2], each below naxes (read before the call
+ *          returns).
+ *   pos    device int32 [naxes][ld_pos], ld_pos >= T, or 0: one row of positions for
+ *          all axes.  A row with a position outside
+ *          [0, max_pos) on any axis is padding: its row of y is not written.
+ * With rot == 0 axes, pos and cos_sin are not read.  Other arguments and errors as
+ * above; naxes > 4 -> ERR_RANGE; naxes < 1, another ld_pos or an axis >= naxes ->
+ * ERR_SHAPE; axes NULL -> ERR_NULL.
+ */
+fp8sm_status fp8sm_qk_norm_rope_axes(const void* x, fp8sm_dtype in, int64_t T, int32_t Hq,
+                                     int32_t Hk, int32_t D, int64_t ld_x, const void* q_weight,
+                                     const void* k_weight, float eps, const float* cos_sin,
+                                     int64_t max_pos, const int32_t* pos, int64_t ld_pos,
+                                     int32_t naxes, const uint8_t* axes, int32_t rot,
+                                     uint32_t flags, void* y, int64_t ld_y, hipStream_t stream);
+
+/*
  * Quantise new keys and values into the cache.  For each touched block, head,
  * and K or V, with a' = max(max|x|, 1e-10) over the block's new values:
  *   e = ceil(log2(RN32(a' / 448))), code = E4M3(clamp(x 2^-e, +-448)),
@@ -486,6 +507,35 @@ fp8sm_status fp8sm_attention_cache(const void* q, int64_t ld_q, fp8sm_dtype in, 
  * invalid input: the call itself reports it). */
 size_t fp8sm_attention_cache_workspace(int64_t T, int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
                                        int64_t max_q, int64_t max_kv, int32_t window);
+
+/*
+ * Attention of whole prompts over their own 16-bit keys and values, before (or
+ * without) a cache: prompt b's tokens are the rows cu[b] .. cu[b+1]-1 of q, k, v and o,
+ *   o[row, h] = sum_t softmax_t(scale q[row, h] . k[t]) v[t]
+ * with the keys and values of head h / (Hq / Hkv), over the prompt's tokens t; with
+ * FP8SM_ATTN_CAUSAL only up to the row's own, with window > 0 (causal only) only the
+ * `window` last of those.  Statistics and sums are fp32; the probabilities are rounded
+ * to the inputs' type for the product with v (half a step of each, in fp16 2^-32 of the
+ * row's largest where that is more).  What a row does not see does not reach it, whatever it
+ * holds; an infinite or NaN value that it sees makes that channel of it infinite or
+ * NaN.  Scores beyond fp32's range come out infinite or NaN.  No gradients.
+ *   q, k, v, o  device bf16/fp16 [T][ld]: Hq, Hkv, Hkv, Hq heads of D values (e.g.
+ *         columns of one projection's rows); 16-byte aligned, ld multiples of 8, ld_k
+ *         and ld_v <= 2^23.  Hq a multiple of Hkv; D is 64 or 128.  o may be q (with
+ *         ld_o == ld_q), other overlaps are not allowed.
+ *   cu    device int32 [nseq+1], non-decreasing, clamped to [0, T]; prompts without
+ *         tokens are allowed, rows of no prompt are left as they were.
+ *   lse   device fp32 [T][Hq] or NULL: ln of the sum of exp(scores).
+ * Errors: T, nseq < 0, heads < 1, Hq % Hkv, window < 0, a scale that is not finite, ld
+ * below a row's length -> ERR_SHAPE; D not listed, window without causal, unknown flags
+ * -> ERR_UNSUPPORTED; T > 2^23, nseq > 2^20, heads > 1024, T * Hq > 2^30, ld_k or ld_v
+ * beyond -> ERR_RANGE; alignment -> ERR_ALIGN.  T == 0 or nseq == 0 launches nothing.
+ */
+fp8sm_status fp8sm_attention_packed(const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                                    const void* v, int64_t ld_v, fp8sm_dtype in, int64_t T,
+                                    int64_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                                    const int32_t* cu, float scale, uint32_t flags, int32_t window,
+                                    void* o, int64_t ld_o, float* lse, hipStream_t stream);
 
 /* Bytes needed for the scales of fp8sm_quant_group (0 on invalid input). */
 size_t fp8sm_scale_bytes(fp8sm_scale_fmt fmt, fp8sm_scale_layout lay, int64_t M, int64_t K_out,
