@@ -24,11 +24,7 @@ __device__ __forceinline__ float rowwise_epilogue(float acc, float sa, float sb)
 // Rowwise epilogue variants: EPI_F16 writes fp16 instead of bf16, EPI_BIAS
 // adds bias[c] (a value of the output dtype, widened exactly) in fp32 before
 // the final rounding: out = rnd(RN32(RN32(acc * sa) * sb) + bias).
-// EPI_STEPS keeps the fp32 value before that rounding: otherwise the compiler may
-// join the last product and the conversion to fp16 into one instruction that rounds
-// once (v_fma_mixlo_f16), which differs from the two roundings in 1 of some thousand
-// outputs.
-enum { EPI_F16 = 1, EPI_BIAS = 2, EPI_STEPS = 4 };
+enum { EPI_F16 = 1, EPI_BIAS = 2 };
 
 // Both conversions are the hardware's round-to-nearest-even (overflow to
 // +-inf); the bf16 one (v_cvt_pk_bf16_f32) equals f32_to_bf16_rne for every
@@ -51,7 +47,6 @@ __device__ __forceinline__ float epi_value(float acc, float sa, float sb,
     else
       v = v + __uint_as_float((uint32_t)bias[c] << 16);
   }
-  if constexpr ((EPI & EPI_F16) != 0 && (EPI & EPI_STEPS) != 0) asm("" : "+v"(v));
   return v;
 }
 
@@ -96,9 +91,10 @@ __device__ __forceinline__ void store_row2(uint16_t* __restrict__ C, int64_t ldc
 // Hardware places consecutive workgroups on the 8 XCDs in turn; give each XCD
 // a contiguous range of logical tiles (so tiles sharing A / B panels share an
 // L2), then walk the logical tiles in groups of kGroupM tile rows.
+template <int kGroupM = 8>
 __device__ __forceinline__ void tile_coords(int bid, int nbid, int tiles_m, int tiles_n, int& tm,
                                             int& tn) {
-  constexpr int kXcd = 8, kGroupM = 8;
+  constexpr int kXcd = 8;
   const int xcd = bid % kXcd, idx = bid / kXcd;
   const int lid = xcd * (nbid / kXcd) + min(xcd, nbid % kXcd) + idx;
   const int per_group = kGroupM * tiles_n;

@@ -2,9 +2,7 @@
 // acc = sum_k A[m,k] B[n,k] in int32 on the int8 matrix instructions.
 //
 // The sum is exact (K <= 65536 products of at most 2^14 fit 31 bits), so K may be
-// walked in any order and split over wavefronts: every variant gives the same
-// bits.  A lane's operand of v_mfma_i32_32x32x32_i8 is 16 bytes of a row; which k
-// they are does not matter as long as both operands agree.
+// walked in any order and split over wavefronts: every variant gives the same bits.
 #include "gemm_common.h"
 #include "lds_copy.h"
 
@@ -13,24 +11,87 @@
 
 namespace fp8sm {
 
-typedef int i32x16 __attribute__((ext_vector_type(16)));
-
-__device__ __forceinline__ f32x4 to_f32(int a, int b, int c, int d) {
-  return f32x4{(float)a, (float)b, (float)c, (float)d};
-}
+// Scales and bias of NC (4 or a multiple of 8) consecutive columns, and a row's outputs
+// there: NC / 4 tiles of four sums.  Columns come in eights inside N or outside.
+template <int EPI, int NC>
+struct Columns {
+  float sb[NC], bias[(EPI & EPI_BIAS) != 0 ? NC : 1];
+  __device__ __forceinline__ void load(const float* __restrict__ scales, int vec, const uint16_t* __restrict__ b, int c0, int N) {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int c = min(c0 + (k & ~3), N - 4) + (k & 3);
+      sb[k] = scales[vec ? c : 0];
+      if constexpr ((EPI & EPI_BIAS) != 0)
+        bias[k] = (EPI & EPI_F16) != 0 ? (float)__builtin_bit_cast(_Float16, b[c]) : __uint_as_float((uint32_t)b[c] << 16);
+    }
+  }
+  __device__ __forceinline__ uint32_t pair(int a0, int a1, float sa, int k) const {
+    uint16_t u[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float y = (float)(e ? a1 : a0) * sa;
+      y = y * sb[k + e];
+      if constexpr ((EPI & EPI_BIAS) != 0) y = y + bias[k + e];
+      // Keeps the fp32 value before its rounding: the compiler would join the last
+      // product and the conversion to fp16 into one instruction that rounds once
+      // (v_fma_mixlo_f16), which differs in 1 of some thousand outputs.
+      if constexpr ((EPI & EPI_F16) != 0) asm("" : "+v"(y));
+      u[e] = epi_round<EPI>(y);
+    }
+    return (uint32_t)u[0] | (uint32_t)u[1] << 16;
+  }
+  // `left`: columns from here to N
+  __device__ __forceinline__ void store(uint16_t* __restrict__ C, const i32x4 (&t)[NC / 4], float sa, int left) const {
+    if constexpr (NC == 4) {
+      if (left > 0) *reinterpret_cast<uint2*>(C) = make_uint2(pair(t[0][0], t[0][1], sa, 0), pair(t[0][2], t[0][3], sa, 2));
+    } else {
+#pragma unroll
+      for (int j = 0; j < NC / 4; j += 2)
+        if (4 * j < left)
+          *reinterpret_cast<uint4*>(C + 4 * j) =
+              make_uint4(pair(t[j][0], t[j][1], sa, 4 * j), pair(t[j][2], t[j][3], sa, 4 * j + 2),
+                         pair(t[j + 1][0], t[j + 1][1], sa, 4 * j + 4), pair(t[j + 1][2], t[j + 1][3], sa, 4 * j + 6));
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
-// Tile kernel.  A workgroup computes BM x BN outputs with WM x WN wavefronts; K is
-// walked in chunks of 64 that copies bring into an LDS ring of NSLOT slots (BM rows
-// of A, then BN rows of B), one barrier a chunk.  The barrier that makes chunk k + 1
-// visible comes before chunk k's matrix work; its fragments are read into a second
-// register set while chunk k is multiplied.
+// Tile kernel.  A workgroup computes BM x BN outputs with WM x WN wavefronts.  K is
+// walked in steps of 128, whole 128-byte lines of every row, that copies bring into an
+// LDS ring of NSLOT slots (BM rows of A, then BN rows of B), one barrier a step.  A step
+// is two chunks of 64, each in a register set of its own: one is multiplied while the
+// next is read, and reads and copies are placed between the rows of products.
 //
-// LDS: 16-byte piece c of row r lies at c ^ swizzle(r mod 16), so that consecutive
-// lanes, which read the same piece of consecutive rows, hit distinct banks.
-constexpr int kTileK = 64;
+// 8320 x 21504 x 5376, 256 x 256 tiles: 778 .. 790 us, 2.44 .. 2.47 POPS, where a
+// library int8 product takes 850 .. 865 on the same box.  The same tile measured 1000 us with
+// v_mfma_i32_32x32x32_i8 and steps of 64, 974 with scales read ahead of the stores, 872
+// with 16x16x64 (half the accumulator traffic of an operation), 833 with reads and
+// copies between the products, 812 with a ring walk of 4 tile rows instead of 8, 788
+// with steps of 128 (half the lines that copies touch).  Bound by the chip's power and
+// the copies beside the products: without copies 744 us in the first form, with all
+// codes 0 825 against 972.  Small tiles are bound by the copies' rate, about 30 bytes a
+// clock and CU, which more wavefronts raise (128 x 128: 63 us with 4 wavefronts, 44
+// with 8, at 333 x 5376 x 14336).  Slower, measured: wavefronts of 128 x 128 (895
+// against 833), rings of 3 and 5 slots of 64 (the same, 847), splitting a step's K
+// over two sets of wavefronts (the same).
+//
+// Outputs: B is the first operand of v_mfma_i32_16x16x64_i8, so lane l gets row l % 16
+// and four columns of a 16 x 16 result.  The TN column tiles of a wavefront interleave:
+// operand row 4 g + i of tile j is column 4 TN g + 4 j + i, and lane group g = l / 16
+// ends up with 4 TN consecutive columns, written 16 bytes at a time.
+//
+// LDS: 16-byte piece c of a row lies at c ^ key, a key that differs between the eight
+// rows that eight consecutive lanes read.
+constexpr int kTileK = 128;
 
-__device__ __forceinline__ int swizzle64(int r) { return ((r >> 1) ^ (r >> 3)) & 3; }
+// Waits until at most min(ahead, MOST) chunks of CPW copies are on their way.
+template <int CPW, int MOST>
+__device__ __forceinline__ void wait_ahead(int ahead) {
+  if constexpr (MOST > 0) {
+    if (ahead < MOST) return wait_ahead<CPW, MOST - 1>(ahead);
+  }
+  wait_copies_but<MOST * CPW>();
+}
 
 template <int BM, int BN, int WM, int WN, int NSLOT, int OCC, int EPI>
 __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void gemm_int8_tile_kernel(
@@ -38,14 +99,14 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void gemm_int8_til
     uint16_t* __restrict__ C, int64_t ldc, int M, int N, int K, const float* __restrict__ sa,
     int sa_vec, const float* __restrict__ sb, int sb_vec, const uint16_t* __restrict__ bias,
     int tiles_m, int tiles_n, GemmBatch gb) {
-  constexpr int NW = WM * WN, TM = BM / WM / 32, TN = BN / WN / 32;
+  constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr int SLOT = (BM + BN) * kTileK;
-  constexpr int CPW = SLOT / 1024 / NW;  // copies of a wavefront a chunk: 16 rows of 64 bytes each
-  static_assert(TM * 32 * WM == BM && TN * 32 * WN == BN && CPW * NW * 1024 == SLOT, "tile shape");
+  constexpr int CPW = SLOT / 1024 / NW;  // copies of a wavefront a step: 8 rows of 128 bytes each
+  static_assert(TM * 16 * WM == BM && TN * 16 * WN == BN && CPW * NW * 1024 == SLOT && TM >= 2, "tile shape");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NSLOT * SLOT];
 
   int tm, tn;
-  tile_coords(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
+  tile_coords<4>(blockIdx.x, gridDim.x, tiles_m, tiles_n, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
   {
     const int64_t bi = blockIdx.y;
@@ -57,27 +118,30 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void gemm_int8_til
     M = (int)batch_rows(gb.rows, M);
     if (m0 >= M) return;  // the whole workgroup, before any barrier
   }
-  const int lane = threadIdx.x & 63, x = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & 63, x = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / WN, wn = w % WN;
   const uint32_t lds0 = lds_address(lds);
+  auto key_a = [](int r) { return r & 7; };
+  auto key_b = [](int r) { return (r & 3) | (r / (4 * TN) & 1) << 2; };
 
-  // Copy i of wavefront w brings 16 rows from row 16 (NW i + w) of the slot on; lane l
-  // row l / 4, piece l % 4 of its slot.  Rows past M / N repeat the last one.  A
+  // Copy i of wavefront w brings 8 rows from row 8 (NW i + w) of the slot on; lane l
+  // row l / 8, piece l % 8 of its slot.  Rows past M / N repeat the last one.  A
   // buffer ends at K of its last row: pieces past K of that row come as zeros, those
   // of the others as what follows in memory, and `read` drops both.
   i32x4 rs[CPW];
   uint32_t vo[CPW];
 #pragma unroll
   for (int i = 0; i < CPW; ++i) {
-    const int seg = i * NW + w, r = lane >> 2;
-    const bool isa = seg * 16 < BM;
+    const int seg = i * NW + w, r = lane >> 3;
+    const bool isa = seg * 8 < BM;
     const int64_t ld = isa ? lda : ldb;
-    const int first = isa ? m0 + seg * 16 : n0 + seg * 16 - BM, last = (isa ? M : N) - 1;
+    const int first = isa ? m0 + seg * 8 : n0 + seg * 8 - BM, last = (isa ? M : N) - 1;
     const int r0 = min(first, last), rr = min(first + r, last);
-    // (16 rows of at most 2^24 bytes: below 2^31)
-    rs[i] = raw_buffer((isa ? A : B) + (int64_t)r0 * ld, (uint32_t)((min(first + 15, last) - r0) * ld) + (uint32_t)K);
-    vo[i] = (uint32_t)((rr - r0) * ld) + (uint32_t)(((lane & 3) ^ swizzle64(r)) * 16);
+    const int key = isa ? key_a(r) : key_b(seg * 8 - BM + r);
+    // (8 rows of at most 2^24 bytes: below 2^31)
+    rs[i] = raw_buffer((isa ? A : B) + (int64_t)r0 * ld, (uint32_t)((min(first + 7, last) - r0) * ld) + (uint32_t)K);
+    vo[i] = (uint32_t)((rr - r0) * ld) + (uint32_t)(((lane & 7) ^ key) * 16);
   }
   const int nk = (K + kTileK - 1) / kTileK;
   auto issue = [&](int k) {
@@ -89,96 +153,102 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void gemm_int8_til
 #pragma unroll
     for (int i = 0; i < CPW; ++i) lds_copy16_buf(vo[i] + more, rs[i], soff, slot + (uint32_t)((i * NW + w) * 1024));
   };
-  // waits for the copies of chunk k, `ahead` younger ones may be on their way
+  // Makes step k visible, `ahead` younger ones may be on their way.
   auto arrive = [&](int ahead) {
-    if (NSLOT > 3 && ahead >= 2)
-      wait_copies_but<2 * CPW>();
-    else if (NSLOT > 2 && ahead >= 1)
-      wait_copies_but<CPW>();
-    else
-      wait_copies_but<0>();
+    wait_ahead<CPW, NSLOT - 2>(ahead);
     __syncthreads();
   };
 
-  const int piece0 = ((2 * h) ^ swizzle64(x & 15)) * 16, piece1 = ((2 * h + 1) ^ swizzle64(x & 15)) * 16;
-  const int a_row = (wm * (BM / WM) + x) * kTileK, b_row = (BM + wn * (BN / WN) + x) * kTileK;
-  struct Frag {
-    i32x4 q[2];
+  // A step is two chunks of 64: a lane reads piece 4 half + g of its rows
+  const int a_at = (wm * (BM / WM) + x) * kTileK + 16 * (g ^ key_a(x));
+  const int b_row = wn * (BN / WN) + 4 * TN * (x >> 2) + (x & 3);  // of column tile 0; tile j is 4 j further
+  const int b_at = (BM + b_row) * kTileK + 16 * (g ^ key_b(b_row));
+  auto read_a = [&](int k, int half, int i) {
+    return *reinterpret_cast<const i32x4*>(lds + (k % NSLOT) * SLOT + (a_at ^ (64 * half)) + i * 16 * kTileK);
   };
-  auto read = [&](int k, Frag(&fa)[TM], Frag(&fb)[TN]) {
-    const uint8_t* slot = lds + (k % NSLOT) * SLOT;
+  auto read_b = [&](int k, int half, int j) {
+    return *reinterpret_cast<const i32x4*>(lds + (k % NSLOT) * SLOT + (b_at ^ (64 * half)) + j * 4 * kTileK);
+  };
+  auto read = [&](int k, int half, i32x4(&fa)[TM], i32x4(&fb)[TN]) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      fa[i].q[0] = *reinterpret_cast<const i32x4*>(slot + a_row + i * 32 * kTileK + piece0);
-      fa[i].q[1] = *reinterpret_cast<const i32x4*>(slot + a_row + i * 32 * kTileK + piece1);
-    }
+    for (int j = 0; j < TN; ++j) fb[j] = read_b(k, half, j);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      fb[j].q[0] = *reinterpret_cast<const i32x4*>(slot + b_row + j * 32 * kTileK + piece0);
-      fb[j].q[1] = *reinterpret_cast<const i32x4*>(slot + b_row + j * 32 * kTileK + piece1);
-    }
-    if ((k + 1) * kTileK > K) {  // K % 64 != 0: k past K counts nothing (zeros on one side)
+    for (int i = 0; i < TM; ++i) fa[i] = read_a(k, half, i);
+    if (k * kTileK + 64 * half + 16 * g >= K) {  // past K: counts nothing (zeros on one side)
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-        if (k * kTileK + 32 * h + 16 * p >= K)
-#pragma unroll
-          for (int i = 0; i < TM; ++i) fa[i].q[p] = i32x4{0, 0, 0, 0};
+      for (int j = 0; j < TN; ++j) fb[j] = i32x4{0, 0, 0, 0};
     }
   };
-  i32x16 acc[TM][TN];
+  i32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  auto row = [&](int i, const i32x4(&fa)[TM], const i32x4(&fb)[TN]) {
+#pragma unroll
     for (int j = 0; j < TN; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+  };
+  auto multiply = [&](const i32x4(&fa)[TM], const i32x4(&fb)[TN]) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  // B first: a lane gets four consecutive columns of its output row
-  auto multiply = [&](const Frag(&fa)[TM], const Frag(&fb)[TN]) {
+    for (int i = 0; i < TM; ++i) row(i, fa, fb);
+  };
+  // The same with the reads of another chunk, and copies, beside the rows of products.
+  auto beside = [&](const i32x4(&fa)[TM], const i32x4(&fb)[TN], int k, int half, i32x4(&na)[TM], i32x4(&nb)[TN], int copy, auto with_copies) {
+    const uint32_t to = lds0 + (uint32_t)((copy % NSLOT) * SLOT);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int j = 0; j < TN; ++j)
+        if (j * TM / TN / 2 == i) nb[j] = read_b(k, half, j);
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j].q[p], fa[i].q[p], acc[i][j], 0, 0, 0);
+      for (int q = 0; q < TM; ++q)
+        if (q * (TM - 2) / TM + 1 == i) na[q] = read_a(k, half, q);
+      if constexpr (decltype(with_copies)::value) {
+#pragma unroll
+        for (int q = 0; q < CPW; ++q)
+          if (q * TM / CPW == i) lds_copy16_buf(vo[q], rs[q], copy * kTileK, to + (uint32_t)((q * NW + w) * 1024));
+      }
+      row(i, fa, fb);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
-  Frag fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+  i32x4 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
   for (int k = 0; k < NSLOT - 1 && k < nk; ++k) issue(k);
   arrive(min(NSLOT - 2, nk - 1));
   if (NSLOT - 1 < nk) issue(NSLOT - 1);
-  read(0, fa0, fb0);
-  auto step = [&](int k, const Frag(&fa)[TM], const Frag(&fb)[TN], Frag(&na)[TM], Frag(&nb)[TN]) {
+  read(0, 0, fa0, fb0);
+  int k = 0;
+  for (; k + NSLOT < nk - 1; ++k) {  // neither step k + 1 nor step k + NSLOT is the last
+    beside(fa0, fb0, k, 1, fa1, fb1, 0, std::false_type{});
+    wait_copies_but<(NSLOT - 2) * CPW>();
+    __syncthreads();  // step k + 1 is there, and everybody has read step k
+    beside(fa1, fb1, k + 1, 0, fa0, fb0, k + NSLOT, std::true_type{});
+  }
+  for (; k < nk; ++k) {
+    read(k, 1, fa1, fb1);
+    multiply(fa0, fb0);
     if (k + 1 < nk) {
       arrive(min(NSLOT - 2, nk - 2 - k));
-      if (k + NSLOT < nk) issue(k + NSLOT);  // into chunk k's slot: everybody has read it
-      read(k + 1, na, nb);
+      if (k + NSLOT < nk) issue(k + NSLOT);
+      read(k + 1, 0, fa0, fb0);
     }
-    multiply(fa, fb);
-  };
-  int k = 0;
-  for (; k + 1 < nk; k += 2) {
-    step(k, fa0, fb0, fa1, fb1);
-    step(k + 1, fa1, fb1, fa0, fb0);
+    multiply(fa1, fb1);
   }
-  if (k < nk) step(k, fa0, fb0, fa1, fb1);
 
-  // lane (x, h): row x of each row subtile, columns 8v + 4h .. + 3 of each column
-  // subtile in registers 4v .. 4v + 3
+  // Scales and bias are read before any store (they were not: 21 us of 77 at 333 x 5376 x
+  // 14336), from columns held inside N.
+  const int c0 = n0 + wn * (BN / WN) + 4 * TN * g;
+  Columns<EPI, 4 * TN> col;
+  col.load(sb, sb_vec, bias, c0, N);
+  float sar[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) sar[i] = sa[sa_vec ? min(m0 + wm * (BM / WM) + 16 * i + x, M - 1) : 0];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int r = m0 + wm * (BM / WM) + 32 * i + x;
-    if (r >= M) continue;
-    const float sar = sa[sa_vec ? r : 0];
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int c = n0 + wn * (BN / WN) + 32 * j + 8 * v + 4 * h;
-        if (c >= N) continue;
-        const i32x16& t = acc[i][j];
-        store_row4<EPI>(C, ldc, r, c, to_f32(t[4 * v], t[4 * v + 1], t[4 * v + 2], t[4 * v + 3]), sar, sb, sb_vec, bias);
-      }
+    const int r = m0 + wm * (BM / WM) + 16 * i + x;
+    if (r < M) col.store(C + (int64_t)r * ldc + c0, acc[i], sar[i], N - c0);
   }
 }
 
@@ -187,7 +257,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void gemm_int8_til
 // and that stream is the bound, so operands go straight from memory to registers and
 // the NW wavefronts split K, 256 at a time, each with the next 256 on their way; the
 // partial sums are added in LDS.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes
-// from k = 16 (l / 16) on of row l % 16.
+// from k = 16 (l / 16) on of row l % 16.  16 rows, weights from HBM: 4096 x 4096 7.2
+// us, 14336 x 4096 15.6 us (3.8 TB/s, some 3 us of it the launch).  Streaming
+// (nontemporal) loads of B took 9.1 and 16.7 us: each 128-byte line is read by two of them.
 template <int MT, int NT, int NW, bool TAIL, int EPI>
 __global__ __launch_bounds__(64 * NW) void gemm_int8_few_kernel(
     const uint8_t* __restrict__ A, int64_t lda, const uint8_t* __restrict__ B, int64_t ldb,
@@ -230,7 +302,7 @@ __global__ __launch_bounds__(64 * NW) void gemm_int8_few_kernel(
       int at = k * STEP + 64 * u + 16 * g;
       if constexpr (TAIL) at = min(at, K - 16);  // no branch around a load
 #pragma unroll
-      for (int j = 0; j < NT; ++j) s.b[u][j] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb[j] + at));
+      for (int j = 0; j < NT; ++j) s.b[u][j] = *reinterpret_cast<const i32x4*>(pb[j] + at);
 #pragma unroll
       for (int i = 0; i < MT; ++i) s.a[u][i] = *reinterpret_cast<const i32x4*>(pa[i] + at);
     }
@@ -278,13 +350,15 @@ __global__ __launch_bounds__(64 * NW) void gemm_int8_few_kernel(
   __syncthreads();
   for (int at = threadIdx.x; at < MT * NT * 64; at += 64 * NW) {
     const int tile = at >> 6, l = at & 63;
-    i32x4 sum = part[0][tile][l];
-#pragma unroll
-    for (int v = 1; v < NW; ++v) sum += part[v][tile][l];
     // lane l: row l % 16, columns 4 (l / 16) .. + 3
     const int r = m0 + 16 * (tile / NT) + (l & 15), c = n0 + 16 * (tile % NT) + 4 * (l >> 4);
-    if (r < M && c < N)
-      store_row4<EPI>(C, ldc, r, c, to_f32(sum[0], sum[1], sum[2], sum[3]), sa[sa_vec ? r : 0], sb, sb_vec, bias);
+    Columns<EPI, 4> col;
+    col.load(sb, sb_vec, bias, c, N);
+    const float sar = sa[sa_vec ? min(r, M - 1) : 0];
+    i32x4 sum[1] = {part[0][tile][l]};
+#pragma unroll
+    for (int v = 1; v < NW; ++v) sum[0] += part[v][tile][l];
+    if (r < M) col.store(C + (int64_t)r * ldc + c, sum, sar, N - c);
   }
 }
 
@@ -295,7 +369,7 @@ template <int BM, int BN, int WM, int WN, int NSLOT, int OCC>
 static hipError_t launch_tile(const GemmArgs& g, hipStream_t s) {
   const int tiles_m = (int)((g.M + BM - 1) / BM), tiles_n = (int)((g.N + BN - 1) / BN);
   return with_epi(g, [&](auto e) {
-    hipLaunchKernelGGL((gemm_int8_tile_kernel<BM, BN, WM, WN, NSLOT, OCC, decltype(e)::value | EPI_STEPS>),
+    hipLaunchKernelGGL((gemm_int8_tile_kernel<BM, BN, WM, WN, NSLOT, OCC, decltype(e)::value>),
                        grid2((int64_t)tiles_m * tiles_n, g), dim3(64 * WM * WN), 0, s, g.A, g.lda, g.B, g.ldb, g.C,
                        g.ldc, (int)g.M, (int)g.N, (int)g.K, static_cast<const float*>(g.sa), (int)(g.sa_kind == 1),
                        static_cast<const float*>(g.sb), (int)(g.sb_kind == 2), static_cast<const uint16_t*>(g.bias),
@@ -309,7 +383,7 @@ static hipError_t launch_few(const GemmArgs& g, hipStream_t s) {
                   (unsigned)((g.M + 16 * MT - 1) / (16 * MT)));
   auto go = [&](auto tail) {
     return with_epi(g, [&](auto e) {
-      hipLaunchKernelGGL((gemm_int8_few_kernel<MT, NT, NW, decltype(tail)::value, decltype(e)::value | EPI_STEPS>), grid,
+      hipLaunchKernelGGL((gemm_int8_few_kernel<MT, NT, NW, decltype(tail)::value, decltype(e)::value>), grid,
                          dim3(64 * NW), 0, s, g.A, g.lda, g.B, g.ldb, g.C, g.ldc, (int)g.M, (int)g.N, (int)g.K,
                          static_cast<const float*>(g.sa), (int)(g.sa_kind == 1), static_cast<const float*>(g.sb),
                          (int)(g.sb_kind == 2), static_cast<const uint16_t*>(g.bias), g.batch);
@@ -318,15 +392,45 @@ static hipError_t launch_few(const GemmArgs& g, hipStream_t s) {
   return g.K % 256 ? go(std::true_type{}) : go(std::false_type{});
 }
 
+// Few rows go to the streaming kernel (16 rows, weights from HBM: 4096 x 4096 7.2 us
+// against 9.4 in tiles, 14336 x 4096 15.6 and 16.5; 32 rows: 8.7 and 9.5, but 25 and 17),
+// in panels of 16 columns while 512 workgroups hold them all (5.6 .. 7.2 us for 4096
+// columns, 7.2 .. 8.5 with 32; 14336 columns 19.2 and 15.6).
+//
+// The others go to the tile whose turns cost least: a workgroup per CU and turn, times
+// what a step of 128 measured (in 10 ns, alone in its turn and with others behind it).
+// Over 17 .. 8320 rows of six weights of 1 .. 116 MB this picks within 1% of the fastest tile on
+// average, 15% at worst.
 hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s) {
   // (a launch holds less than 2^32 threads)
-  if (g.M <= 64 && g.N <= (1 << 26)) {
-    if (g.M <= 16) return launch_few<1, 2, 8>(g, s);
-    if (g.M <= 32) return launch_few<2, 2, 8>(g, s);
-    return launch_few<4, 2, 8>(g, s);
+  if (g.M <= 16 && g.N <= 8192) return launch_few<1, 1, 8>(g, s);
+  if (g.M <= 16 && g.N <= (1 << 26)) return launch_few<1, 2, 8>(g, s);
+  if (g.M <= 32 && g.N <= 4096) return launch_few<2, 1, 8>(g, s);
+  struct Tile {
+    int bm, bn, alone, turn;
+  };
+  constexpr Tile tiles[] = {{64, 32, 17, 19}, {64, 64, 22, 22}, {64, 128, 31, 33}, {128, 128, 37, 46}, {256, 256, 125, 150}};
+  int best = 4;
+  int64_t least = INT64_MAX;
+  bool alone = false;
+  for (int i = 4; i >= 0; --i) {
+    const int64_t n = ((g.M + tiles[i].bm - 1) / tiles[i].bm) * ((g.N + tiles[i].bn - 1) / tiles[i].bn);
+    const int64_t turns = (n * g.batch.count + 255) / 256;
+    const int64_t cost = turns == 1 ? tiles[i].alone : turns * tiles[i].turn;
+    if (n <= (1 << 23) && cost < least) {
+      least = cost;
+      best = i;
+      alone = turns == 1;
+    }
   }
-  if (g.M * g.N >= (int64_t)256 * 256 * 256) return launch_tile<256, 256, 2, 4, 4, 1>(g, s);
-  return launch_tile<128, 128, 2, 2, 4, 2>(g, s);
+  switch (best) {
+    case 0: return launch_tile<64, 32, 2, 2, 6, 2>(g, s);
+    case 1: return launch_tile<64, 64, 2, 4, 4, 2>(g, s);
+    case 2: return launch_tile<64, 128, 2, 4, 3, 2>(g, s);
+    case 3:  // two workgroups a CU hide each other's waits; a single one takes a deeper ring
+      return alone ? launch_tile<128, 128, 2, 4, 4, 1>(g, s) : launch_tile<128, 128, 2, 4, 2, 2>(g, s);
+    default: return launch_tile<256, 256, 2, 4, 2, 1>(g, s);
+  }
 }
 
 }  // namespace fp8sm
