@@ -426,7 +426,7 @@ hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s) {
   switch (best) {
     case 0: return launch_tile<64, 32, 2, 2, 6, 2>(g, s);
     case 1: return launch_tile<64, 64, 2, 4, 4, 2>(g, s);
-    case 2: return launch_tile<64, 128, 2, 4, 3, 2>(g, s);
+    case 2: return launch_tile<64, 128, 2, 4, 4, 1>(g, s);
     case 3:  // two workgroups a CU hide each other's waits; a single one takes a deeper ring
       return alone ? launch_tile<128, 128, 2, 4, 4, 1>(g, s) : launch_tile<128, 128, 2, 4, 2, 2>(g, s);
     default: return launch_tile<256, 256, 2, 4, 2, 1>(g, s);
