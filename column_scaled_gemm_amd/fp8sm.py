@@ -586,14 +586,19 @@ def scaled_mm_batched(a, b, sa, sb, kind_a, kind_b, rows=None, c=None, bias=None
 # ---------------------------------------------------------------- 8-bit integers
 
 def _batched(t, what):
-    """(batches, rows, columns, batch stride, row stride) of a matrix or a batch of them."""
-    _unit_last(t, what)
-    if t.dim() == 2:
-        return 1, t.shape[0], t.shape[1], 0, _ld(t)
-    if t.dim() != 3:
-        raise ValueError(f"{what}: needs 2 or 3 dimensions, got {tuple(t.shape)}")
-    B, M, K = t.shape
-    return B, M, K, _bs(t, B), _ld(t)
+    """(batches, rows, columns, batch stride, row stride) of a matrix or a batch of
+    them, with strides that the layout rules accept where they address nothing."""
+    sh, st = t.shape, t.stride()
+    n = len(sh)
+    if n != 2 and n != 3:
+        raise ValueError(f"{what}: needs 2 or 3 dimensions, got {tuple(sh)}")
+    if st[-1] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    M, K = sh[-2:]
+    ld = st[-2] if M > 1 and K else -(-K // 16) * 16
+    if n == 2:
+        return 1, M, K, 0, ld
+    return sh[0], M, K, st[0] if sh[0] > 1 and M and K else 0, ld
 
 
 def quant_int8(x, fuse_silu_mul=False, rows=None, q=None, scales=None, stream=None):
@@ -608,17 +613,17 @@ def quant_int8(x, fuse_silu_mul=False, rows=None, q=None, scales=None, stream=No
     K = K_in // 2 if fuse_silu_mul else K_in
     if fuse_silu_mul and K_in % 2:
         raise ValueError("x: fuse_silu_mul needs [gate | up], an even number of columns")
-    lead = x.shape[:-1]
     if q is None:
-        q = torch.empty(lead + (K,), dtype=torch.int8, device=x.device)
+        q = torch.empty(x.shape[:-1] + (K,), dtype=torch.int8, device=x.device)
     else:
-        _holds(q, lead + (K,), "q", torch.int8)
+        _holds(q, x.shape[:-1] + (K,), "q", torch.int8)
     _, _, _, bs_q, ld_q = _batched(q, "q")
     if scales is None:
-        scales = torch.empty(lead, dtype=torch.float32, device=x.device)
+        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     else:
         _holds_bytes(scales, 4 * B * M, "scales", torch.float32)
-    rows = _rows_arg(rows, B)
+    if rows is not None:
+        rows = _rows_arg(rows, B)
     st, px, pr, pq, ps = _on_current(x, rows, q, scales)
     st = _load().fp8sm_quant_int8(px, _dtype_code(x), B, M, K, bs_x, ld_x, pr,
                                   FUSE_SILU_MUL if fuse_silu_mul else 0, pq, bs_q, ld_q, ps, st)
@@ -661,7 +666,8 @@ def scaled_mm_int8(a, b, sa, sb, kind_a=KIND_ROW, kind_b=KIND_COL, rows=None, c=
         raise TypeError("sa and sb must be float32")
     bs_sa = _scale_batch_stride(sa, kind_a, B, 1 if kind_a == KIND_TENSOR else M, "sa")
     bs_sb = _scale_batch_stride(sb, kind_b, B, 1 if kind_b == KIND_TENSOR else N, "sb")
-    rows = _rows_arg(rows, B)
+    if rows is not None:
+        rows = _rows_arg(rows, B)
     st, pa, pr, pb, pc, psa, psb, pbias = _on_current(a, rows, b, c, sa, sb, bias)
     st = _load().fp8sm_scaled_mm_int8(B, pr, pa, bs_a, lda, pb, bs_b, ldb, pc, bs_c, ldc, M, N, K,
                                       kind_a, psa, bs_sa, kind_b, psb, bs_sb, pbias, out, st)
