@@ -87,14 +87,29 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
   // leaves: products beside exponentials, not both on the same (8320 tokens, 56 heads:
   // 988 -> 962 us).  The lowest bit of a wavefront's slot on its SIMD tells them apart.
   if (__builtin_amdgcn_s_getreg((4 - 1) << 11 | 4) & 1) __builtin_amdgcn_s_setprio(1);  // (HW_ID, bits 0 .. 3)
-  // The list is head, row tile with the last tile (most tokens to see) first, each
-  // XCD taking a contiguous part where that leaves none with more work.
+  // A head's row tiles come with the last one (most tokens to see) first.  The list has
+  // the heads side by side, which leaves the short tiles of all heads for its end; with a
+  // multiple of eight heads each XCD reads the keys of its own ones.  Against the heads
+  // one behind the other: 14 heads of 64 in 7 prompts 88 -> 76 us, 20 heads, 4160 tokens
+  // 174 -> 114, 24 heads 141 -> 128, 56 heads, 8320 tokens 998 -> 1018 in one run, 1020 ->
+  // 1014 in another.  Beyond 64 heads the keys of so many outgrow an XCD's L2 (112 heads,
+  // 8320 tokens: 1940 us so, 2200 side by side); there they follow each other, each XCD
+  // taking a contiguous part.  Prompts ordered by length too: 73 us and 990, but up to
+  // 46% slower with many prompts, whose tiles of one length share no keys.
   const int64_t slots = packed_slots(a), n = slots * a.heads, id = workgroup_id();
   if (id >= n) return;
-  const int64_t part = n >> 3, rest = n & 7;
-  const int64_t at = a.heads % 8 == 0 || a.heads >= 64 ? (id & 7) * part + min(id & 7, rest) + (id >> 3) : id;
-  const int hk = (int)(at / slots);
-  const int64_t slot = slots - 1 - (at - hk * slots);
+  int64_t from_last, hk64;
+  if (a.heads <= 64) {
+    from_last = id / a.heads;
+    hk64 = id - from_last * a.heads;
+  } else {
+    const int64_t part = n >> 3, rest = n & 7;
+    const int64_t at = (id & 7) * part + min(id & 7, rest) + (id >> 3);
+    hk64 = at / slots;
+    from_last = at - hk64 * slots;
+  }
+  const int hk = (int)hk64;
+  const int64_t slot = slots - 1 - from_last;
   // (the prompts have no cache: their lengths stand in for cached ones, unused)
   const KvBatch kb{a.cu, a.cu + 1, nullptr, 0, 1, a.T, a.B};
   const Seq s = find_seq(kb, 0, slot, a.G, 7, 1);

@@ -89,6 +89,12 @@ def test_flat_sharp_and_negative_scores(gain, scale, dtype):
     run([190, 40], 2, 1, 64, dtype, gain=gain, scale=scale)
 
 
+@pytest.mark.parametrize("Hq,H", [(63, 63), (64, 64), (65, 65), (72, 72), (140, 70)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_heads(Hq, H, causal):
+    run([140, 0, 30, 1], Hq, H, 64, "bf16", causal=causal, before=3)
+
+
 def test_rows_before_the_first_prompt():
     run([100, 30], 4, 2, 128, "bf16", before=5)
     run([100, 30], 4, 2, 64, "fp16", before=300)
