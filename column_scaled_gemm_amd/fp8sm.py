@@ -125,6 +125,8 @@ def _check(status, where):
 # The raw handle of the current stream without building a Stream object (3 us of
 # host time a call, measured), where torch offers it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device where a tensor of some device shows that there is one.
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None):
@@ -156,7 +158,7 @@ def _on_current(*tensors):
     device is asked for once)."""
     if not tensors[0].is_cuda:
         _ptr(tensors[0])
-    cur = torch.cuda.current_device()
+    cur = _device_now()
     out = [_raw_stream(cur) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream]
     for t in tensors:
         out.append(None if t is None else t.data_ptr() if t.get_device() == cur else _ptr(t))
@@ -745,15 +747,15 @@ def quant_group_scatter(x, dst, R, fmt=SCALE_UE8M0_BYTE, layout=LAYOUT_MN_MAJOR,
 def _head_rows(t, heads, head_dim, what):
     """A [T, heads, D] view with the heads side by side, or a [T, heads * D]
     matrix -> (rows, row stride in elements)."""
-    sh = t.shape
+    sh, st = t.shape, t.stride()
     if len(sh) == 3:
-        ok = sh[1] == heads and sh[2] == head_dim and (heads == 1 or t.stride(1) == head_dim)
+        ok = sh[1] == heads and sh[2] == head_dim and (heads == 1 or st[1] == head_dim)
     else:
         ok = len(sh) == 2 and sh[1] == heads * head_dim
-    if not ok or t.stride(-1) != 1:
+    if not ok or st[-1] != 1:
         raise ValueError(f"{what}: needs [T, {heads}, {head_dim}] or [T, {heads * head_dim}] with each "
-                         f"row's heads side by side, got {tuple(sh)}, strides {t.stride()}")
-    return sh[0], (t.stride(0) if sh[0] > 1 else heads * head_dim)
+                         f"row's heads side by side, got {tuple(sh)}, strides {st}")
+    return sh[0], (st[0] if sh[0] > 1 else heads * head_dim)
 
 
 def _out_rows(t, T, heads, head_dim, dtype, what):
