@@ -128,18 +128,6 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
   const int tok = ok ? r / a.G : 0, head = hk * a.G + (ok ? r - tok * a.G : 0);
   const int see_hi = ok ? (a.causal ? tok + 1 : s.n) : 0;
   const int see_lo = a.window ? max(tok - a.window + 1, 0) : 0;
-  uint4 qf[NK];
-  {
-    const uint16_t* q = a.q + (int64_t)(s.c0 + tok) * a.ld_q + (int64_t)head * D;
-    const uint32_t flip = a.negate ? 0x80008000u : 0u;
-#pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (ok) v = *reinterpret_cast<const uint4*>(q + 16 * k + 8 * h);
-      v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-      qf[k] = v;
-    }
-  }
   // what the wavefront's rows see: nothing outside [w_lo, w_hi), everything inside
   // [all_lo, all_hi)
   int w_lo = 0, w_hi = 0, all_lo = 0, all_hi = 0;
@@ -193,6 +181,22 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
 #pragma unroll
     for (int c = 0; c < CPW; ++c) lds_copy16_buf(voff[c], rv, 0, dst + TILE + (uint32_t)(4 * c + w) * 1024);
   };
+
+  // The first copies leave before the queries are asked for, and those of lanes without
+  // a row come from the tile's first one: one trip to memory for all.
+  issue(0);
+  uint4 qf[NK];
+  {
+    const uint16_t* q = a.q + (int64_t)(s.c0 + tok) * a.ld_q + (int64_t)head * D;
+    const uint32_t flip = a.negate ? 0x80008000u : 0u, keep = ok ? ~0u : 0u;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) qf[k] = *reinterpret_cast<const uint4*>(q + 16 * k + 8 * h);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      qf[k].x = (qf[k].x ^ flip) & keep, qf[k].y = (qf[k].y ^ flip) & keep;
+      qf[k].z = (qf[k].z ^ flip) & keep, qf[k].w = (qf[k].w ^ flip) & keep;
+    }
+  }
 
   // The lane's key row of 32 tokens: row m of the matrix tile is token
   // 16 ((m >> 2) & 1) + 4 (m >> 3) + m % 4, which leaves lane half h with the
@@ -361,7 +365,6 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int k = 0; k < 16; ++k) o[d][k] = 0.f;
-    issue(0);
     if constexpr (decltype(clear_tag)::value) {
       masked(0, steps, clear_tag);
     } else {
@@ -376,7 +379,10 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
     }
   };
   walk(std::false_type{});
-  if (__builtin_amdgcn_readfirstlane(__syncthreads_or(odd))) walk(std::true_type{});
+  if (__builtin_amdgcn_readfirstlane(__syncthreads_or(odd))) {
+    issue(0);
+    walk(std::true_type{});
+  }
 
   const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
   const float sum = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
