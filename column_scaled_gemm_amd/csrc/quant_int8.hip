@@ -8,15 +8,14 @@
 namespace fp8sm {
 
 // silu(g) = RN32(g / RN32(1 + RN32(e^-g))), the library's definition, computed: e^-g in
-// fp64 (x = n ln 2 + r, |r| <= ln 2 / 2, and the series of e^r to r^12: the next term is
-// below 2^-52) and rounded to fp32 once.
+// fp64 (x = n ln 2 + r, |r| < 0.35, and the series of e^r to r^11: the next term is below
+// 2^-47, and so is what fp64's ln 2 lacks, 216 times) and rounded to fp32 once, but for
+// values below 2^-126, which 1 takes in.
 __device__ __forceinline__ float silu(float g) {
-  const double x = fmin(fmax(-(double)g, -150.0), 150.0);  // (e^+-150 is 0 or infinite in fp32)
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  double r = __builtin_fma(n, -0.6931471805599453, x);
-  r = __builtin_fma(n, -2.3190468138462996e-17, r);
-  double p = 1.0 / 479001600.0;
-  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  const float x = fminf(fmaxf(-g, -150.f), 150.f);  // (e^+-150 is 0 or infinite in fp32)
+  const float n = __builtin_rintf(x * 1.442695f);
+  const double r = __builtin_fma((double)n, -0.6931471805599453, (double)x);
+  double p = 1.0 / 39916800.0;
   p = __builtin_fma(p, r, 1.0 / 3628800.0);
   p = __builtin_fma(p, r, 1.0 / 362880.0);
   p = __builtin_fma(p, r, 1.0 / 40320.0);
@@ -28,7 +27,7 @@ __device__ __forceinline__ float silu(float g) {
   p = __builtin_fma(p, r, 0.5);
   p = __builtin_fma(p, r, 1.0);
   p = __builtin_fma(p, r, 1.0);
-  const float e = (float)__builtin_ldexp(p, (int)n);
+  const float e = __builtin_ldexpf((float)p, (int)n);
   return g / (1.0f + e);
 }
 
