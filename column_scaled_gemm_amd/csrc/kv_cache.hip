@@ -60,7 +60,8 @@ constexpr int kRopeU = 4;  // (8320 rows of 112 heads: 1: 119 us, 2: 108, 4: 100
 
 //
 // AXES: pair i turns by row pos[axis(i)][t].  The token's rot cosines and sines are
-// gathered into LDS once for the workgroup's heads.
+// gathered into LDS once for the workgroup's heads, while their first reads are on the
+// way: 8320 rows of 112 heads on three axes take 86.5 us, 5.57 TB/s, as on one axis.
 template <bool F16, int D, bool NORM, bool INTER, bool AXES>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
   constexpr int LPH = D / 8, HPW = 64 / LPH;

@@ -1,5 +1,10 @@
 // Per-token int8 quant for gfx950, optionally of silu(gate) * up:
 //   a' = max(max|y|, 1e-10), scale = RN32(a' / 127), q = RNE(RN32(y * RN32(127 / a'))).
+//
+// Rows are read once and held.  Plain rows are bound by memory: 8320 x 5376 bf16 21.8 us,
+// 6.2 TB/s read and written (a large copy: 5.1).  Of silu(gate) * up the arithmetic
+// bounds, 3.3 .. 3.6 TB/s (8320 x 2048 25 us, 4096 x 7168 44): timing copies without the
+// series of e^-g take 66% of the time, without the exact division 90%.
 #include "device_common.h"
 #include "launch.h"
 
@@ -81,7 +86,6 @@ __device__ __forceinline__ float finite_or_zero(float a) {  // of an absolute va
 
 // W wavefronts (1 or 4) share a row and hold it in registers, NC chunks of eight
 // values a lane; chunks past the row's end read its last one and count for nothing.
-// Bound by memory.
 template <bool F16, bool FUSED, int W, int NC>
 __global__ __launch_bounds__(256) void quant_int8_kernel(QuantInt8Args a) {
   __shared__ float top[4], odd[4];
