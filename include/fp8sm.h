@@ -19,7 +19,9 @@
  * Number format: OCP FP8 E4M3FN codes, one byte each (max 448, no infinities,
  * 0x7F / 0xFF are NaN) -- the input type required in [P1] Summary.  gfx950
  * converts to and from this format natively; the gfx94x FNUZ variant that
- * [P4] Modifications 3 warns about is not supported.
+ * [P4] Modifications 3 warns about is not supported.  A second format, signed 8-bit
+ * integers with a scale per token and per channel, has calls of its own ("8-bit
+ * integers" below).
  */
 #ifndef FP8SM_H
 #define FP8SM_H
