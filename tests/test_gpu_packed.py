@@ -95,6 +95,18 @@ def test_many_heads(Hq, H, causal):
     run([140, 0, 30, 1], Hq, H, 64, "bf16", causal=causal, before=3)
 
 
+def test_more_threads_than_32_bits_count():
+    """300000 prompts without tokens around one with some: 4.9e9 threads in one call."""
+    print("[case] many empty prompts", flush=True)
+    n, H, D = 40, 64, 64
+    q, k, v = (normal(rng(5), n, H, D).bfloat16() for _ in range(3))
+    want = fp8sm.attention_packed(q, k, v, ints([0, n]))
+    for place in (1, 150000, 300000):
+        cu = torch.full((300001,), n, dtype=torch.int32, device="cuda")
+        cu[:place] = 0
+        assert torch.equal(fp8sm.attention_packed(q, k, v, cu), want)
+
+
 def test_rows_before_the_first_prompt():
     run([100, 30], 4, 2, 128, "bf16", before=5)
     run([100, 30], 4, 2, 64, "fp16", before=300)
