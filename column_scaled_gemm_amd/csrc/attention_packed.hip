@@ -19,17 +19,21 @@
 // take both operands in one type, and V is not moved to another one.  The sum l takes
 // the unrounded p.
 //
-// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 960 .. 1010 us, 0.98 .. 1.03 PFLOP/s,
-// where a bf16 library product of 16384^3 reaches 1.36.  Bound by the chip's power: the
-// clock is 1.94 GHz under this load (all zeros: 2.4 GHz and 806 us in as many cycles), of
-// which the matrix pipe is busy 49% and vector instructions 44%.  What the parts cost
-// (timing copies without them): copies 13%, exponentials 10%, LDS reads 9%, the second
-// product 17%.  On the way: 1081 us with values tested for infinities at each of a
-// masked step's products, 1050 with one test a step and keys read four fragments ahead,
-// 1004 with P packed in pairs, 988 with the second walk apart, 962 with priorities.
-// Slower, measured: 64 rows a wavefront, one a SIMD (1470), 256 rows a workgroup (977),
-// rings of three steps (986), 64 rows a workgroup (1382), the next step's scores between
-// this step's exponentials (the registers of two steps' scores spill).
+// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 938 .. 949 us, 1.05 PFLOP/s, where
+// a bf16 library product of 16384^3 reaches 1.36.  Bound by the chip's power, the clock
+// falls below 2 GHz under this load, and by the matrix pipe (32 products of 32 clocks a step
+// and wavefront) beside the vector instructions (about 900 clocks alone, a third of them
+// the 32 exponentials): a SIMD's wavefronts have to be at different ones.  What the
+// parts cost (timing copies without them): copies 13%, exponentials 10%, LDS reads 9%, the
+// second product 17%.  On the way: 1081 us with values tested for infinities at each of
+// a masked step's products, 1050 with one test a step and keys read four fragments
+// ahead, 1004 with P packed in pairs, 988 with the second walk apart, 949 with the
+// wavefronts' priorities, 938 with values read three fragments ahead (960 .. 995 before
+// the last two, by the box).  Slower, measured: 64 rows a wavefront, one a SIMD
+// (1470), 256 rows a workgroup (977 against 962), rings of three steps (986), 64 rows a
+// workgroup (1382), the next step's scores between this step's exponentials (the
+// registers of two steps' scores spill), halves of 32 tokens with exponentials between
+// the products (1046 against 1025), copies sent off behind the first reads (967 against 944).
 #include "attn_common.h"
 #include "lds_copy.h"
 
@@ -41,7 +45,7 @@ typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kPackedRows = 128, kPackedStep = 64;  // rows a workgroup, 32 a wavefront; tokens a step
-constexpr int kAhead = 4;        // fragments of keys on their way to the registers
+constexpr int kAhead = 4, kAheadV = 3;  // fragments of keys, of values on their way to the registers
 
 template <bool F16>
 __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
@@ -83,10 +87,6 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][TILE];
   const int lane = threadIdx.x & 63, x = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Two workgroups share a CU.  Where one's wavefronts go first, the other's fill what it
-  // leaves: products beside exponentials, not both on the same (8320 tokens, 56 heads:
-  // 988 -> 962 us).  The lowest bit of a wavefront's slot on its SIMD tells them apart.
-  if (__builtin_amdgcn_s_getreg((4 - 1) << 11 | 4) & 1) __builtin_amdgcn_s_setprio(1);  // (HW_ID, bits 0 .. 3)
   // A head's row tiles come with the last one (most tokens to see) first.  The list has
   // the heads side by side, which leaves the short tiles of all heads for its end; with a
   // multiple of eight heads each XCD reads the keys of its own ones.  Against the heads
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
   // are infinite or NaN are taken out of the product, see `odd`.
   auto compute = [&](int i, auto partial_tag, auto clear_tag) __attribute__((always_inline)) {
     constexpr bool PARTIAL = decltype(partial_tag)::value, CLEAR = decltype(clear_tag)::value;
-    constexpr int KF = 2 * NK, VF = 4 * DT, VA = kAhead / 2;  // fragments of keys, of values; of those ahead
+    constexpr int KF = 2 * NK, VF = 4 * DT, VA = kAheadV;  // fragments of keys, of values; of those ahead
     const int t0 = t_begin + i * kPackedStep;
     const uint8_t* lk = ring[i & 1][0];
     const uint8_t* lv = ring[i & 1][1];
@@ -246,6 +246,11 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
 #pragma unroll
     for (int f = 0; f < VA; ++f) read_v(f);
 
+    // A SIMD has wavefronts of two or three workgroups.  One that is at its exponentials
+    // goes first: the products of another need an issue slot in eight only, and the other
+    // way round the vector instructions wait for products (8320 tokens, 56 heads: 995 us
+    // without, 949 so, 979 with products first, 988 with one workgroup first throughout).
+    __builtin_amdgcn_s_setprio(2);
     float mx = -INFINITY;
 #pragma unroll
     for (int grp = 0; grp < 2; ++grp) {
@@ -314,6 +319,7 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
         odd |= __any(max(most[0], most[1]) >= (F16 ? 0x7C00 : 0x7F80));
       }
     }
+    __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int f = 0; f < VF; ++f) {
       if (f + VA < VF) read_v(f + VA);

@@ -616,12 +616,12 @@ def quant_int8(x, fuse_silu_mul=False, rows=None, q=None, scales=None, stream=No
     if fuse_silu_mul and K_in % 2:
         raise ValueError("x: fuse_silu_mul needs [gate | up], an even number of columns")
     if q is None:
-        q = torch.empty(x.shape[:-1] + (K,), dtype=torch.int8, device=x.device)
+        q = x.new_empty(x.shape[:-1] + (K,), dtype=torch.int8)
     else:
         _holds(q, x.shape[:-1] + (K,), "q", torch.int8)
     _, _, _, bs_q, ld_q = _batched(q, "q")
     if scales is None:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scales = x.new_empty(x.shape[:-1], dtype=torch.float32)
     else:
         _holds_bytes(scales, 4 * B * M, "scales", torch.float32)
     if rows is not None:
@@ -654,7 +654,7 @@ def scaled_mm_int8(a, b, sa, sb, kind_a=KIND_ROW, kind_b=KIND_COL, rows=None, c=
         out_dtype = c.dtype if c is not None else torch.bfloat16
     out = {torch.bfloat16: BF16, torch.float16: FP16}[out_dtype]
     if c is None:
-        c = torch.empty(a.shape[:-1] + (N,), dtype=out_dtype, device=a.device)
+        c = a.new_empty(a.shape[:-1] + (N,), dtype=out_dtype)
     else:
         _holds(c, a.shape[:-1] + (N,), "c")
     _, _, _, bs_c, ldc = _batched(c, "c")
@@ -800,7 +800,7 @@ def _rope_args(x, q_heads, k_heads, head_dim, cos_sin, q_weight, k_weight, out):
     _unit_last(x, "x")
     _holds(x, (T, row), "x")
     if out is None:
-        out = torch.empty((T, row), dtype=x.dtype, device=x.device)
+        out = x.new_empty((T, row))
     elif out is not x:
         _unit_last(out, "out")
         _holds(out, (T, row), "out", x.dtype)
@@ -1057,14 +1057,14 @@ def attention_packed(q, k, v, cu, scale=None, causal=True, window=0, out=None, l
     if cu.dim() != 1 or cu.numel() < 1 or not cu.is_contiguous():
         raise ValueError("cu: needs [prompts + 1], contiguous")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty((T, Hq, D))
         ld_o = Hq * D
     else:
         ld_o = _out_rows(out, T, Hq, D, q.dtype, "out")
     if lse is not None:
         _holds_bytes(lse, 4 * T * Hq, "lse", torch.float32)
     elif return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
     st, pq, pk, pv, pc, po, pe = _on_current(q, k, v, cu, out, lse)
     st = _load().fp8sm_attention_packed(pq, ld_q, pk, ld_k, pv, ld_v, _dtype_code(q), T, cu.numel() - 1, Hq,
                                         H, D, pc, D ** -0.5 if scale is None else scale,
