@@ -157,7 +157,9 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
   // pairs of pieces (16 channels) at pair ^ vkey(r).
   const uint32_t lds0 = lds_address(&ring[0][0][0]);
   auto kkey = [](int r) __attribute__((always_inline)) {
-    return (r & 3) | (r >> 4 & 1) << 2 | (D == 128 ? (r >> 2 & 1) << 3 : 0);
+    // (16 lanes read at a time, of rows 8 g + {0 .. 7, 16 .. 23}: all 64 banks; rows of 64
+    // channels lie two to a line of banks)
+    return D == 128 ? (r & 3) | (r >> 4 & 1) << 2 | (r >> 2 & 1) << 3 : (r >> 1 & 3) | (r >> 4 & 1) << 2;
   };
   auto vkey = [](int r) __attribute__((always_inline)) { return D == 128 ? (r & 3) | (r & 1) << 2 : r & 3; };
   uint32_t koff[CPW], voff[CPW];
