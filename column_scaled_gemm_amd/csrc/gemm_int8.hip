@@ -70,10 +70,11 @@ struct Columns {
 // with steps of 128 (half the lines that copies touch).  Bound by the chip's power and
 // the copies beside the products: without copies 744 us in the first form, with all
 // codes 0 825 against 972.  Small tiles are bound by the copies' rate, about 30 bytes a
-// clock and CU, which more wavefronts raise (128 x 128: 63 us with 4 wavefronts, 44
-// with 8, at 333 x 5376 x 14336).  Slower, measured: wavefronts of 128 x 128 (895
-// against 833), rings of 3 and 5 slots of 64 (the same, 847), splitting a step's K
-// over two sets of wavefronts (the same).
+// clock and CU, which more wavefronts raise (333 x 5376 x 14336 in tiles of 128 x 128: 63
+// us with 4 wavefronts, 44 with 8; of 64 x 128 39, of 128 x 64 38).  Slower, measured:
+// wavefronts of 128 x 128 (895 against 833), rings of 3 and 5 slots of 64 (the same,
+// 847), splitting a step's K over two sets of wavefronts (the same), six slots for the
+// tiles of 64 and 128 (39.9 against 39.2).
 //
 // Outputs: B is the first operand of v_mfma_i32_16x16x64_i8, so lane l gets row l % 16
 // and four columns of a 16 x 16 result.  The TN column tiles of a wavefront interleave:
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void gemm_int8_til
     multiply(fa1, fb1);
   }
 
-  // Scales and bias are read before any store (they were not: 21 us of 77 at 333 x 5376 x
+  // Scales and bias are read before any store (they were not, in the first form: 21 us of 77 at 333 x 5376 x
   // 14336), from columns held inside N.
   const int c0 = n0 + wn * (BN / WN) + 4 * TN * g;
   Columns<EPI, 4 * TN> col;
@@ -400,7 +401,9 @@ static hipError_t launch_few(const GemmArgs& g, hipStream_t s) {
 // The others go to the tile whose turns cost least: a workgroup per CU and turn, times
 // what a step of 128 measured (in 10 ns, alone in its turn and with others behind it).
 // Over 17 .. 8320 rows of six weights of 1 .. 116 MB this picks within 1% of the fastest tile on
-// average, 15% at worst.
+// average, 15% at worst.  Of the two tiles of 128 and 64, the one with 128 rows has half as
+// many workgroups read each weight (300 x 5376 x 14336: 42.0 us against 38.0), the other
+// wastes less of a few rows (150 rows: 26.1 and 34.4).
 hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s) {
   // (a launch holds less than 2^32 threads)
   if (g.M <= 16 && g.N <= 8192) return launch_few<1, 1, 8>(g, s);
@@ -409,11 +412,12 @@ hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s) {
   struct Tile {
     int bm, bn, alone, turn;
   };
-  constexpr Tile tiles[] = {{64, 32, 17, 19}, {64, 64, 22, 22}, {64, 128, 31, 33}, {128, 128, 37, 46}, {256, 256, 125, 150}};
-  int best = 4;
+  constexpr Tile tiles[] = {{64, 32, 17, 19}, {64, 64, 22, 22}, {64, 128, 31, 33},
+                            {128, 64, 29, 31}, {128, 128, 37, 46}, {256, 256, 125, 150}};
+  int best = 5;
   int64_t least = INT64_MAX;
   bool alone = false;
-  for (int i = 4; i >= 0; --i) {
+  for (int i = 5; i >= 0; --i) {
     const int64_t n = ((g.M + tiles[i].bm - 1) / tiles[i].bm) * ((g.N + tiles[i].bn - 1) / tiles[i].bn);
     const int64_t turns = (n * g.batch.count + 255) / 256;
     const int64_t cost = turns == 1 ? tiles[i].alone : turns * tiles[i].turn;
@@ -427,7 +431,8 @@ hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s) {
     case 0: return launch_tile<64, 32, 2, 2, 6, 2>(g, s);
     case 1: return launch_tile<64, 64, 2, 4, 4, 2>(g, s);
     case 2: return launch_tile<64, 128, 2, 4, 4, 1>(g, s);
-    case 3:  // two workgroups a CU hide each other's waits; a single one takes a deeper ring
+    case 3: return launch_tile<128, 64, 4, 2, 4, 1>(g, s);
+    case 4:  // two workgroups a CU hide each other's waits; a single one takes a deeper ring
       return alone ? launch_tile<128, 128, 2, 4, 4, 1>(g, s) : launch_tile<128, 128, 2, 4, 2, 2>(g, s);
     default: return launch_tile<256, 256, 2, 4, 2, 1>(g, s);
   }

@@ -22,7 +22,7 @@ def exact(a, b, sa, sb, bias, out):
 
 # rows and columns that lead to each tile of the dispatch, and to its edges
 KINDS = {"few16": ((1, 16), (8, 9000)), "few32": ((17, 32), (8, 4096)), "64x32": ((33, 128), (8, 4096)),
-         "64x64": ((33, 64), (5000, 16000)), "64x128": ((65, 400), (4000, 9000)),
+         "64x64": ((33, 64), (5000, 16000)), "64x128": ((65, 400), (4000, 9000)), "128x64": ((257, 384), (4600, 5376)),
          "128x128": ((200, 900), (1000, 6000)), "128x128 many": ((1500, 2500), (2000, 4200)),
          "256x256": ((2500, 3500), (5000, 9000))}
 
