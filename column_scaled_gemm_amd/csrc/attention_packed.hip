@@ -19,13 +19,13 @@
 // take both operands in one type, and V is not moved to another one.  The sum l takes
 // the unrounded p.
 //
-// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 938 .. 949 us, 1.05 PFLOP/s, where
+// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 938 .. 972 us, 1.02 .. 1.06 PFLOP/s, where
 // a bf16 library product of 16384^3 reaches 1.36.  Bound by the chip's power, the clock
 // falls below 2 GHz under this load, and by the matrix pipe (32 products of 32 clocks a step
 // and wavefront) beside the vector instructions (about 900 clocks alone, a third of them
 // the 32 exponentials): a SIMD's wavefronts have to be at different ones.  What the
-// parts cost (timing copies without them): copies 13%, exponentials 10%, LDS reads 9%, the
-// second product 17%.  On the way: 1081 us with values tested for infinities at each of
+// parts cost (timing copies without them, before the priorities): copies 13%,
+// exponentials 10%, LDS reads 9%, the second product 17%.  On the way: 1081 us with values tested for infinities at each of
 // a masked step's products, 1050 with one test a step and keys read four fragments
 // ahead, 1004 with P packed in pairs, 988 with the second walk apart, 949 with the
 // wavefronts' priorities, 938 with values read three fragments ahead (960 .. 995 before
