@@ -53,7 +53,7 @@ def listed():
         dict(name="attn_texts", op="attn", B=13, lo=0, hi=3001, mix=3, Hq=32, Hkv=8, D=128, causal=True,
              window=0, dtype="bf16"),
         # patches of pictures of different sizes, each seeing its whole picture
-        dict(name="attn_pictures", op="attn", B=7, lo=256, hi=2500, mix=4, Hq=14, Hkv=14, D=64, causal=False,
+        dict(name="attn_pictures", op="attn", B=7, lo=256, hi=2500, mix=4, Hq=16, Hkv=16, D=64, causal=False,
              window=0, dtype="fp16"),
     ]
 
