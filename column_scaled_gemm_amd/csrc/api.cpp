@@ -489,6 +489,10 @@ fp8sm_status fp8sm_scaled_mm_int8(int64_t nbatch, const int32_t* rows, const int
                         GemmBatch{nbatch, bs_a, bs_b, bs_c, bs_sa, bs_sb, rows}, MM_INT8);
 }
 
+const char* fp8sm_int8_kernel(int64_t nbatch, int64_t M, int64_t N) {
+  return int8_kernel_name(pick_int8_kernel(nbatch, M, N));
+}
+
 fp8sm_status fp8sm_quant_int8(const void* x, fp8sm_dtype in, int64_t nbatch, int64_t M,
                               int64_t K_out, int64_t bs_x, int64_t ld_x, const int32_t* rows,
                               uint32_t flags, int8_t* q, int64_t bs_q, int64_t ld_q,

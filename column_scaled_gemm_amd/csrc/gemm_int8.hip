@@ -404,36 +404,62 @@ static hipError_t launch_few(const GemmArgs& g, hipStream_t s) {
 // average, 15% at worst.  Of the two tiles of 128 and 64, the one with 128 rows has half as
 // many workgroups read each weight (300 x 5376 x 14336: 42.0 us against 38.0), the other
 // wastes less of a few rows (150 rows: 26.1 and 34.4).
-hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s) {
-  // (a launch holds less than 2^32 threads)
-  if (g.M <= 16 && g.N <= 8192) return launch_few<1, 1, 8>(g, s);
-  if (g.M <= 16 && g.N <= (1 << 26)) return launch_few<1, 2, 8>(g, s);
-  if (g.M <= 32 && g.N <= 4096) return launch_few<2, 1, 8>(g, s);
+enum { INT8_FEW_16X16, INT8_FEW_16X32, INT8_FEW_32X16, INT8_64X32, INT8_64X64, INT8_64X128, INT8_128X64,
+       INT8_128X128_ALONE, INT8_128X128, INT8_256X256 };
+
+int pick_int8_kernel(int64_t batches, int64_t M, int64_t N) {
+  if (M <= 16 && N <= 8192) return INT8_FEW_16X16;
+  if (M <= 16 && N <= (1 << 26)) return INT8_FEW_16X32;
+  if (M <= 32 && N <= 4096) return INT8_FEW_32X16;
   struct Tile {
-    int bm, bn, alone, turn;
+    int id, bm, bn, alone, turn;
   };
-  constexpr Tile tiles[] = {{64, 32, 17, 19}, {64, 64, 22, 22}, {64, 128, 31, 33},
-                            {128, 64, 29, 31}, {128, 128, 37, 46}, {256, 256, 125, 150}};
-  int best = 5;
+  constexpr Tile tiles[] = {{INT8_64X32, 64, 32, 17, 19},     {INT8_64X64, 64, 64, 22, 22},
+                            {INT8_64X128, 64, 128, 31, 33},   {INT8_128X64, 128, 64, 29, 31},
+                            {INT8_128X128, 128, 128, 37, 46}, {INT8_256X256, 256, 256, 125, 150}};
+  int best = INT8_256X256;
   int64_t least = INT64_MAX;
-  bool alone = false;
   for (int i = 5; i >= 0; --i) {
-    const int64_t n = ((g.M + tiles[i].bm - 1) / tiles[i].bm) * ((g.N + tiles[i].bn - 1) / tiles[i].bn);
-    const int64_t turns = (n * g.batch.count + 255) / 256;
-    const int64_t cost = turns == 1 ? tiles[i].alone : turns * tiles[i].turn;
-    if (n <= (1 << 23) && cost < least) {
+    const Tile& t = tiles[i];
+    const int64_t n = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    const int64_t turns = (n * batches + 255) / 256;
+    const int64_t cost = turns == 1 ? t.alone : turns * t.turn;
+    // (a launch holds less than 2^32 threads, a workgroup up to 512; 256 x 256 always fits)
+    if (n < (1 << 23) && cost < least) {
       least = cost;
-      best = i;
-      alone = turns == 1;
+      // two workgroups a CU hide each other's waits; a single one takes a deeper ring
+      best = t.id == INT8_128X128 && turns == 1 ? INT8_128X128_ALONE : t.id;
     }
   }
-  switch (best) {
-    case 0: return launch_tile<64, 32, 2, 2, 6, 2>(g, s);
-    case 1: return launch_tile<64, 64, 2, 4, 4, 2>(g, s);
-    case 2: return launch_tile<64, 128, 2, 4, 4, 1>(g, s);
-    case 3: return launch_tile<128, 64, 4, 2, 4, 1>(g, s);
-    case 4:  // two workgroups a CU hide each other's waits; a single one takes a deeper ring
-      return alone ? launch_tile<128, 128, 2, 4, 4, 1>(g, s) : launch_tile<128, 128, 2, 4, 2, 2>(g, s);
+  return best;
+}
+
+const char* int8_kernel_name(int id) {
+  switch (id) {
+    case INT8_FEW_16X16: return "few 16x16";
+    case INT8_FEW_16X32: return "few 16x32";
+    case INT8_FEW_32X16: return "few 32x16";
+    case INT8_64X32: return "64x32";
+    case INT8_64X64: return "64x64";
+    case INT8_64X128: return "64x128";
+    case INT8_128X64: return "128x64";
+    case INT8_128X128_ALONE: return "128x128 alone";
+    case INT8_128X128: return "128x128";
+    default: return "256x256";
+  }
+}
+
+hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s) {
+  switch (pick_int8_kernel(g.batch.count, g.M, g.N)) {
+    case INT8_FEW_16X16: return launch_few<1, 1, 8>(g, s);
+    case INT8_FEW_16X32: return launch_few<1, 2, 8>(g, s);
+    case INT8_FEW_32X16: return launch_few<2, 1, 8>(g, s);
+    case INT8_64X32: return launch_tile<64, 32, 2, 2, 6, 2>(g, s);
+    case INT8_64X64: return launch_tile<64, 64, 2, 4, 4, 2>(g, s);
+    case INT8_64X128: return launch_tile<64, 128, 2, 4, 4, 1>(g, s);
+    case INT8_128X64: return launch_tile<128, 64, 4, 2, 4, 1>(g, s);
+    case INT8_128X128_ALONE: return launch_tile<128, 128, 2, 4, 4, 1>(g, s);
+    case INT8_128X128: return launch_tile<128, 128, 2, 4, 2, 2>(g, s);
     default: return launch_tile<256, 256, 2, 4, 2, 1>(g, s);
   }
 }

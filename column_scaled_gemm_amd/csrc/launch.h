@@ -129,6 +129,8 @@ hipError_t launch_gemm_blockwise(const GemmArgs& g, hipStream_t s);
 hipError_t launch_gemm_rowwise_fp8mfma(const GemmArgs& g, hipStream_t s);
 // int8 codes in A and B, rowwise / per-tensor scales.
 hipError_t launch_gemm_int8(const GemmArgs& g, hipStream_t s);
+int pick_int8_kernel(int64_t batches, int64_t M, int64_t N);  // the one it launches
+const char* int8_kernel_name(int id);
 // One matrix instruction on host-supplied register images (probe.hip).
 hipError_t launch_mfma_probe(int instr, const uint32_t* a, const uint32_t* b, float* d,
                              hipStream_t s);

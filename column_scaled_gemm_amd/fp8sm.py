@@ -77,6 +77,7 @@ SIGNATURES = {
     "fp8sm_variant_count": (_int, []),
     "fp8sm_variant_name": (ctypes.c_char_p, [_int]),
     "fp8sm_pick_variant": (_int, [_i64, _i64, _i64]),
+    "fp8sm_int8_kernel": (ctypes.c_char_p, [_i64, _i64, _i64]),
     "fp8sm_variant_accepts": (_int, [_int, _i64, _i64, _i64]),
     "fp8sm_scaled_mm_fp8mfma": (_int, [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _int, _p,
                                        _int, _p, _p]),
@@ -197,6 +198,11 @@ def variant_name(vid):
 
 def pick_variant(M, N, K):
     return _load().fp8sm_pick_variant(M, N, K)
+
+
+def int8_kernel(nbatch, M, N):
+    """Name of the kernel that scaled_mm_int8 takes for a size."""
+    return _load().fp8sm_int8_kernel(nbatch, M, N).decode()
 
 
 def variant_accepts(vid, M, N, K):

@@ -561,6 +561,10 @@ const char* fp8sm_variant_name(int id);
 /* Variant the dispatch table picks for a shape (no launch, no validation). */
 int fp8sm_pick_variant(int64_t M, int64_t N, int64_t K);
 
+/* Test hook: name of the kernel that fp8sm_scaled_mm_int8 takes for a size, its rows x
+ * columns a workgroup (no launch, no validation). */
+const char* fp8sm_int8_kernel(int64_t nbatch, int64_t M, int64_t N);
+
 /* Test hook: 1 if variant `id` computes rowwise/per-tensor calls of this
  * shape, else 0 (a forced variant that does not is ERR_UNSUPPORTED).  The
  * decode variants bound M (32 or 64); the tile variants take any shape
