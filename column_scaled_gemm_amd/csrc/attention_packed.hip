@@ -36,6 +36,7 @@
 // the products (1046 against 1025), copies sent off behind the first reads (967 against 944).
 #include "attn_common.h"
 #include "lds_copy.h"
+#include "packed_rows.h"
 
 #include <type_traits>
 
@@ -123,9 +124,9 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
   const int steps = (t_end - t_begin + kPackedStep - 1) / kPackedStep;
 
   // the lane's row, and what it sees: [see_lo, see_hi)
-  const int r = r0 + 32 * w + x;
-  const bool ok = r < rows;
-  const int tok = ok ? r / a.G : 0, head = hk * a.G + (ok ? r - tok * a.G : 0);
+  const PackedRow own = packed_row(r0, 32 * w + x, rows, hk, a.G);
+  const bool ok = own.ok;
+  const int tok = own.tok, head = own.head;
   const int see_hi = ok ? (a.causal ? tok + 1 : s.n) : 0;
   const int see_lo = a.window ? max(tok - a.window + 1, 0) : 0;
   // what the wavefront's rows see: nothing outside [w_lo, w_hi), everything inside
