@@ -99,7 +99,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeArgs a) {
     const int h = min(h0 + u * HPW, heads - 1);
     v[u] = load_stream16(x + (int64_t)h * D + lh * 8);
   }
-  __shared__ float turns[AXES ? D : 1];
+  __shared__ __attribute__((aligned(16))) float turns[AXES ? D : 1];
   if constexpr (AXES) {
     if ((int)threadIdx.x < a.rot) turns[threadIdx.x] = gathered;
     __syncthreads();
