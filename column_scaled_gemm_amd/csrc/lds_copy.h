@@ -1,6 +1,6 @@
-// Copies from memory straight into LDS, 16 bytes a lane, for the kernels that keep
-// an LDS ring (gfx950).  Inline asm, so that the compiler does not wait for every
-// copy before each LDS read; wait_copies waits for what is needed.  lds is the
+// Copies from memory straight into LDS, 16 bytes a lane, for the LDS rings of the int8
+// product and the packed attention (gfx950).  Inline asm, so that the compiler does not wait for every
+// copy before each LDS read; wait_copies_but waits for what is needed.  lds is the
 // wave-uniform LDS byte address of lane 0's destination, lane i writes lds + 16 i.
 // m0 is used for nothing else in these kernels; a copy that follows its write
 // needs one wait state, which inside inline asm nobody else puts in.
@@ -13,13 +13,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// from a lane's own address
-__device__ __forceinline__ void lds_copy16(const void* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(lds), "v"(g)
-               : "memory", "m0");
-}
 // from a raw buffer: base of rsrc + voff (a lane's) + soff
 __device__ __forceinline__ void lds_copy16_buf(uint32_t voff, i32x4 rsrc, int soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
