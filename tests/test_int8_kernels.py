@@ -36,3 +36,30 @@ def test_a_launch_holds_less_than_2_to_32_threads():
             name = fp8sm.int8_kernel(batches, M, N)
             n, threads = workgroups(name, M, N)
             assert n * threads < 1 << 32, (batches, M, N, name)
+
+
+# (batches, rows, columns) that reach each kernel, its ring's slots (0: no ring)
+SIZES = {"few 16x16": ((1, 13, 4104), (5, 16, 264)), "few 16x32": ((1, 9, 8200), (1, 16, 9000)),
+         "few 32x16": ((1, 31, 2056), (4, 20, 520)), "64x32": ((1, 100, 4000), (1, 492, 1000)),
+         "64x64": ((1, 48, 9000), (3, 200, 1000)), "64x128": ((1, 140, 9000), (1, 190, 9000)),
+         "128x64": ((1, 300, 5376), (1, 100, 14336)), "128x128 alone": ((1, 600, 4104), (2, 90, 8200)),
+         "128x128": ((1, 2560, 6656), (2, 1700, 5000)), "256x256": ((1, 3406, 7544), (3, 700, 5000))}
+SLOTS = {"64x32": 6, "64x64": 4, "64x128": 4, "128x64": 4, "128x128 alone": 4, "128x128": 2, "256x256": 2}
+
+
+def lengths(name):
+    """K at which a kernel's walk has one step, as many as its ring, more, and tails."""
+    if name not in SLOTS:                       # eight wavefronts, 256 of K a step
+        return 16, 2048, 3 * 2048, 3 * 2048 + 16, 2 * 2048 + 240
+    ring = 128 * SLOTS[name]
+    return 16, ring, ring + 128, ring + 5 * 128, ring + 5 * 128 + 16, ring + 4 * 128 + 112
+
+
+@pytest.mark.parametrize("name", SIZES)
+def test_the_sizes_that_are_tested_reach_the_kernel_they_name(name):
+    """tests/test_gpu_int8_kernels.py runs these."""
+    from column_scaled_gemm_amd import fp8sm
+    for size in SIZES[name]:
+        assert fp8sm.int8_kernel(*size) == name, size
+    # the loop that copies, reads and multiplies at once runs from two steps more than slots on
+    assert name not in SLOTS or sum(-(-K // 128) >= SLOTS[name] + 2 for K in lengths(name)) >= 3
