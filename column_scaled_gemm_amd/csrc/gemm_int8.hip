@@ -258,8 +258,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC * WM * WN / 4) void gemm_int8_til
 // and that stream is the bound, so operands go straight from memory to registers and
 // the NW wavefronts split K, 256 at a time, each with the next 256 on their way; the
 // partial sums are added in LDS.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes
-// from k = 16 (l / 16) on of row l % 16.  16 rows, weights from HBM: 4096 x 4096 7.2
-// us, 14336 x 4096 15.6 us (3.8 TB/s, some 3 us of it the launch).  Streaming
+// from k = 16 (l / 16) on of row l % 16.  16 rows, weights from HBM: 4096 x 4096 7.3
+// us, 14336 x 4096 15.6 .. 16.3 us (3.7 TB/s, some 3 us of it the launch; 14.4 where the
+// last-level cache holds the 59 MB).  Streaming
 // (nontemporal) loads of B took 9.1 and 16.7 us: each 128-byte line is read by two of them.
 template <int MT, int NT, int NW, bool TAIL, int EPI>
 __global__ __launch_bounds__(64 * NW) void gemm_int8_few_kernel(
@@ -393,10 +394,14 @@ static hipError_t launch_few(const GemmArgs& g, hipStream_t s) {
   return g.K % 256 ? go(std::true_type{}) : go(std::false_type{});
 }
 
-// Few rows go to the streaming kernel (16 rows, weights from HBM: 4096 x 4096 7.2 us
-// against 9.4 in tiles, 14336 x 4096 15.6 and 16.5; 32 rows: 8.7 and 9.5, but 25 and 17),
-// in panels of 16 columns while 512 workgroups hold them all (5.6 .. 7.2 us for 4096
-// columns, 7.2 .. 8.5 with 32; 14336 columns 19.2 and 15.6).
+// Few rows go to the streaming kernel, in panels of 16 columns while the whole batch has
+// one for each CU at most; then up to 16 rows in panels of 32 columns, 17 .. 32 rows in
+// tiles.  Weights from HBM, us in panels of 16 and in what follows: 16 rows x 4096 x 7168
+// 10.6 and 12.8, 16 x 4352 x 4096 10.6 and 8.8 (1 row 8.3 and 7.5), 16 x 8192 x 8192 19.0
+// and 16.9 (1 row 15.4 and 16.6), 32 experts of 16 x 7168 x 2048 137 and 110 (1 row 105
+// and 87); 32 x 4096 x 7168 13.7 and 14.7, two of them 23.6 and 16.1, 32 experts of 32 x
+// 4096 x 2048 106 and 55.  Tiles for up to 16 rows lie between 20% faster than panels of
+// 32 columns (16 rows, K of 2048, more than 1800 panels) and 19% slower (1 row, K of 4096).
 //
 // The others go to the tile whose turns cost least: a workgroup per CU and turn, times
 // what a step of 128 measured (in 10 ns, alone in its turn and with others behind it).
@@ -408,9 +413,10 @@ enum { INT8_FEW_16X16, INT8_FEW_16X32, INT8_FEW_32X16, INT8_64X32, INT8_64X64, I
        INT8_128X128_ALONE, INT8_128X128, INT8_256X256 };
 
 int pick_int8_kernel(int64_t batches, int64_t M, int64_t N) {
-  if (M <= 16 && N <= 8192) return INT8_FEW_16X16;
+  const bool one_each = (N + 15) / 16 * batches <= 256;  // panels of 16 columns, CUs
+  if (M <= 16 && one_each) return INT8_FEW_16X16;
   if (M <= 16 && N <= (1 << 26)) return INT8_FEW_16X32;
-  if (M <= 32 && N <= 4096) return INT8_FEW_32X16;
+  if (M <= 32 && one_each) return INT8_FEW_32X16;
   struct Tile {
     int id, bm, bn, alone, turn;
   };

@@ -39,7 +39,7 @@ def test_a_launch_holds_less_than_2_to_32_threads():
 
 
 # (batches, rows, columns) that reach each kernel, its ring's slots (0: no ring)
-SIZES = {"few 16x16": ((1, 13, 4104), (5, 16, 264)), "few 16x32": ((1, 9, 8200), (1, 16, 9000)),
+SIZES = {"few 16x16": ((1, 13, 4088), (5, 16, 264)), "few 16x32": ((1, 9, 8200), (1, 16, 9000)),
          "few 32x16": ((1, 31, 2056), (4, 20, 520)), "64x32": ((1, 100, 4000), (1, 492, 1000)),
          "64x64": ((1, 48, 9000), (3, 200, 1000)), "64x128": ((1, 140, 9000), (1, 190, 9000)),
          "128x64": ((1, 300, 5376), (1, 100, 14336)), "128x128 alone": ((1, 600, 4104), (2, 90, 8200)),
@@ -63,3 +63,14 @@ def test_the_sizes_that_are_tested_reach_the_kernel_they_name(name):
         assert fp8sm.int8_kernel(*size) == name, size
     # the loop that copies, reads and multiplies at once runs from two steps more than slots on
     assert name not in SLOTS or sum(-(-K // 128) >= SLOTS[name] + 2 for K in lengths(name)) >= 3
+
+
+def test_panels_of_16_columns_count_the_batch():
+    """They serve calls whose panels are a CU's one workgroup at most: a batch has its
+    panels side by side in the same launch (32 experts of 16 rows x 7168 columns: 14336)."""
+    from column_scaled_gemm_amd import fp8sm
+    for M, panel in ((1, "few 16x16"), (16, "few 16x16"), (17, "few 32x16"), (32, "few 32x16")):
+        for batches, N in ((1, 4096), (2, 2048), (32, 128), (256, 16), (256, 8), (5, 816)):
+            assert fp8sm.int8_kernel(batches, M, N) == panel, (batches, M, N)
+        for batches, N in ((1, 4104), (2, 2056), (32, 136), (32, 7168), (257, 8), (65535, 8), (8, 4096)):
+            assert fp8sm.int8_kernel(batches, M, N) != panel, (batches, M, N)
