@@ -88,19 +88,13 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[2][2][TILE];
   const int lane = threadIdx.x & 63, x = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // A head's row tiles come with the last one (most tokens to see) first.  The list has
-  // the heads side by side, which leaves the short tiles of all heads for its end; with a
-  // multiple of eight heads each XCD reads the keys of its own ones.  Against the heads
-  // one behind the other: 14 heads of 64 in 7 prompts 88 -> 76 us, 20 heads, 4160 tokens
-  // 174 -> 114, 24 heads 141 -> 128, 56 heads, 8320 tokens 998 -> 1018 in one run, 1020 ->
-  // 1014 in another.  Beyond 64 heads the keys of so many outgrow an XCD's L2 (112 heads,
-  // 8320 tokens: 1940 us so, 2200 side by side); there they follow each other, each XCD
-  // taking a contiguous part.  Prompts ordered by length too: 73 us and 990, but up to
-  // 46% slower with many prompts, whose tiles of one length share no keys.
+  // The list of workgroups: prompts ordered by length too took 73 us against 76 (14 heads of
+  // 64 in 7 prompts) and 990 against 1014 (8320 tokens), but up to 46% more with many prompts,
+  // whose tiles of one length share no keys.
   const int64_t slots = packed_slots(a), n = slots * a.heads, id = workgroup_id();
   if (id >= n) return;
   int64_t from_last, hk64;
-  if (a.heads <= 64) {
+  if (a.side) {
     from_last = id / a.heads;
     hk64 = id - from_last * a.heads;
   } else {
@@ -411,7 +405,8 @@ __global__ __launch_bounds__(256, 2) void attn_packed_kernel(PackedArgs a) {
 }
 
 template <bool F16, int D>
-static void packed_launch(const PackedArgs& a, hipStream_t s) {
+static void packed_launch(PackedArgs a, hipStream_t s) {
+  a.side = heads_side_by_side(a.T, a.B, a.heads, D);
   attn_packed_kernel<F16, D><<<grid_of(packed_slots(a) * a.heads), 256, 0, s>>>(a);
 }
 

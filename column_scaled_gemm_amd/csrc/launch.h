@@ -242,6 +242,7 @@ struct PackedArgs {
   int T, B, Hq, heads, G, D;  // heads: of keys and values
   float scale_log2;           // |softmax scale| * log2(e), above 0
   int negate, causal, window;
+  int side = 0;  // set at the launch: the heads side by side in the list of workgroups
 };
 hipError_t launch_attention_packed(const PackedArgs& a, bool f16, hipStream_t s);
 
