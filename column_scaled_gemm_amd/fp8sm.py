@@ -7,6 +7,7 @@ torch.empty.  The library is loaded on first use; if it is missing or fails to
 load, every call raises -- there is no fallback.
 """
 import ctypes
+import operator
 import os
 from typing import NamedTuple
 
@@ -833,6 +834,9 @@ def rope_axes(sections, mixed=False):
     """The axis of each pair of a head, for qk_norm_rope_axes: sections[a] pairs of
     axis a, one section behind the other, or with mixed=True in turn while they last
     (0, 1, 2, 0, 1, 2, ..)."""
+    sections = [operator.index(n) for n in sections]
+    if any(n < 0 for n in sections):
+        raise ValueError(f"sections: numbers of pairs, got {sections}")
     if not mixed:
         return [a for a, n in enumerate(sections) for _ in range(n)]
     left, axes = list(sections), []
