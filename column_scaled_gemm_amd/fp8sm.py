@@ -866,7 +866,7 @@ def qk_norm_rope_axes(x, q_heads, k_heads, head_dim, positions, cos_sin, axes, q
         raise TypeError("positions must be int32")
     n = positions.shape[0]
     if not isinstance(axes, bytes):
-        axes = bytes(axes)
+        axes = bytes(list(axes))
     if len(axes) != rot // 2:
         raise ValueError(f"axes: needs the axis of each of {rot // 2} pairs, got {len(axes)}")
     st, px, pq, pk, pc, pp, po = _on_current(x, q_weight, k_weight, cos_sin, positions, out)
