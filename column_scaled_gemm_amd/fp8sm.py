@@ -398,8 +398,9 @@ def _rows_arg(rows, B):
     """Device int32 [B] live-row counts, or None."""
     if rows is None:
         return None
-    if rows.dtype != torch.int32 or rows.dim() != 1 or rows.numel() != B or not rows.is_cuda:
-        raise ValueError("rows must be a device int32 tensor with one count per batch")
+    if rows.dtype != torch.int32 or rows.dim() != 1 or rows.numel() != B or not rows.is_cuda \
+            or not rows.is_contiguous():
+        raise ValueError("rows must be a contiguous device int32 tensor with one count per batch")
     return rows
 
 
