@@ -19,7 +19,7 @@
 // take both operands in one type, and V is not moved to another one.  The sum l takes
 // the unrounded p.
 //
-// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 938 .. 972 us, 1.02 .. 1.06 PFLOP/s, where
+// 8320 tokens, 56 heads of 128, causal (0.99 TFLOP): 932 .. 972 us, 1.02 .. 1.06 PFLOP/s, where
 // a bf16 library product of 16384^3 reaches 1.36.  Bound by the chip's power, the clock
 // falls below 2 GHz under this load, and by the matrix pipe (32 products of 32 clocks a step
 // and wavefront) beside the vector instructions (about 900 clocks alone, a third of them
